@@ -8,6 +8,11 @@
  *   kvq_decode_int4   unified_attention_int4 / _attn_packed (split-KV) + log-sum-exp merge
  *   kvq_decode_tq     triton_turboquant_decode_attention / _tq_decode_stage1 (KEY_FP8) + merge
  *   kvq_fwht128       fwht128_quant_fp8 / _fwht_quant_kernel
+ * and, for the steps around them and for layers kept in 16 bits or FP8 (no counterpart on the pages):
+ *   kvq_plan_step     block tables and slot maps from the requests' lengths
+ *   kvq_rope          rotary positions
+ *   kvq_write_kv      rotary positions + write into a 16-bit or FP8 paged cache
+ *   kvq_decode_kv     split paged decode attention over that cache
  *
  * Conventions shared by every call
  *   - Every pointer argument is a DEVICE pointer owned by the caller (kvq_copy_async also takes
@@ -52,7 +57,8 @@ typedef enum {
   KVQ_ERR_CUDA = 5          /* a CUDA runtime call or kernel launch failed                */
 } kvq_status;
 
-typedef enum { KVQ_BF16 = 0, KVQ_F16 = 1, KVQ_F32 = 2 } kvq_dtype;
+/* KVQ_E4M3 (FP8 E4M3FN) is a cache type of kvq_paged_kv only. */
+typedef enum { KVQ_BF16 = 0, KVQ_F16 = 1, KVQ_F32 = 2, KVQ_E4M3 = 3 } kvq_dtype;
 
 /* Static, human-readable name of a status. Never NULL. */
 KVQ_API const char *kvq_status_string(kvq_status status);
@@ -395,6 +401,172 @@ KVQ_API kvq_status kvq_fwht128(const void *x, uint8_t *y_e4m3, float *row_scale,
                        kvq_stream_t stream);
 
 /*
+ * kvq_plan_step -- the block tables and slot maps of one serving step, built on the GPU from the
+ * requests' lengths. Request b has context_lens[b] tokens in the cache and brings query_lens[b] new
+ * ones; its blocks are the first entries of row rows[b] of a persistent block table. With
+ *   L_b = context + query, have_b = ceil(context / block_size), need_b = ceil(L_b / block_size):
+ *   block_table[rows[b]][j] = free_blocks[*cursor + sum_{a<b} (need_a - have_a) + j - have_b]
+ *                                                                  for have_b <= j < need_b
+ *   *cursor_out = *cursor + sum_b (need_b - have_b)      (free blocks taken so far)
+ *   seq_lens[b] = L_b;  query_start_loc[b] = sum_{a<b} query_a  (B + 1 entries)
+ *   token i of request b, row t = query_start_loc[b] + i: p = context_lens[b] + i, positions[t] = p,
+ *     slot_mapping[t] = block_table[rows[b]][p / block_size] * block_size + p % block_size
+ *   batch_table[b][j] = block_table[rows[b]][j] for j < need_b (the other entries stay as they were)
+ * Rows of positions and slot_mapping behind the last token are set to -1, which every write skips.
+ *
+ *   context_lens  int32 [B].   query_lens  int32 [B], or NULL: one new token each.
+ *   rows          int32 [B], all different, or NULL: request b is row b.
+ *   block_table   int32 [num_rows, max_blocks], extended in place.
+ *   free_blocks   int32 [num_free], ids in the order they are handed out, with cursor int64 [1]; or
+ *                 NULL (cursor and cursor_out NULL too): the table already holds every block.
+ *   cursor_out    int64 [1]; may be cursor itself (then a second, one-block kernel advances it).
+ *   seq_lens [B], query_start_loc [B + 1], positions [T] int32, slot_mapping int64 [T],
+ *   batch_table   int32 [B, max_blocks]; each may be NULL (not wanted). T: rows of positions and slot_mapping.
+ *   B at most 8192 (KVQ_ERR_UNSUPPORTED above). Outputs do not overlap each other or the inputs.
+ * Device flags: 1 for a row outside [0, num_rows) (its tokens get slot -1, it takes no block) or an id
+ * outside [0, num_blocks) (a new entry becomes -1; its tokens get slot -1); 2 for a negative length
+ * (read as 0), a sequence above max_blocks blocks (seq_lens is clamped, the tokens behind get slot -1)
+ * or more than T tokens (those behind row T are not written); 32 when the free list runs out (entries -1,
+ * slots -1, the cursor stops at num_free).
+ */
+KVQ_API kvq_status kvq_plan_step(const int32_t *context_lens, const int32_t *query_lens, const int32_t *rows,
+                                 int32_t *block_table, int32_t max_blocks, int64_t num_rows,
+                                 const int32_t *free_blocks, int64_t num_free, const int64_t *cursor,
+                                 int64_t *cursor_out, int32_t *seq_lens, int32_t *query_start_loc,
+                                 int32_t *positions, int64_t *slot_mapping, int32_t *batch_table, int32_t B,
+                                 int32_t T, int32_t block_size, int64_t num_blocks, kvq_stream_t stream);
+
+/*
+ * kvq_rotary -- rotary positions. Pair i < rotary_dim / 2 of a head turns by positions[t] * f_i:
+ *   (a, b) -> attn_factor * (a cos - b sin, b cos + a sin)
+ * where the pair is elements (i, i + rotary_dim / 2) or, interleaved, (2i, 2i + 1); elements from
+ * rotary_dim on pass unchanged. f_i is given as a fraction of a full turn for each position, in
+ * units of 2^-64 turns, so that positions[t] * f_i modulo a turn is exact integer arithmetic and the
+ * angle is as good at position 10^6 as at 10. The rotation is fp32, rounded once.
+ *
+ *   positions    int32 [T]; a token with a position < 0 is padding: nothing of it is written.
+ *   freqs        uint64 [rotary_dim / 2] (device), from kvq_rope_frequencies or the caller's own.
+ *   rotary_dim   even, 2 .. D.   attn_factor  finite (1 without a long-context scaling that sets it).
+ */
+typedef struct kvq_rotary {
+  const int32_t *positions;
+  const uint64_t *freqs;
+  int32_t rotary_dim;
+  int32_t interleaved;
+  float attn_factor;
+} kvq_rotary;
+
+/*
+ * kvq_rope_frequencies -- fills a HOST array with the freqs of kvq_rotary and *attn_factor. With
+ * f_i = base^(-2i / rotary_dim) radians a position, scaling NULL or of kind
+ *   KVQ_ROPE_NONE    f_i
+ *   KVQ_ROPE_LINEAR  f_i / factor
+ *   KVQ_ROPE_BANDS   by the turns t_i = original f_i / 2 pi that a pair makes over the original context:
+ *                    f_i (r + (1 - r) / factor), r = clamp((t_i - low) / (high - low), 0, 1)
+ *   KVQ_ROPE_YARN    f_i ((1 - r_i) + r_i / factor), r_i = clamp((i - i_high) / max(i_low - i_high, 0.001), 0, 1),
+ *                    i_x the pair that makes x turns over the original context, rotary_dim ln(original / (2 pi x)) /
+ *                    (2 ln base), i_high rounded down and at least 0, i_low rounded up and at most
+ *                    rotary_dim - 1; attn_factor = 0.1 ln(factor) + 1
+ * low / high: turns; 0 for the usual ones (BANDS 1 and 4, YARN 1 and 32). attn_factor is 1 but for YARN.
+ */
+typedef enum { KVQ_ROPE_NONE = 0, KVQ_ROPE_LINEAR = 1, KVQ_ROPE_BANDS = 2, KVQ_ROPE_YARN = 3 } kvq_rope_kind;
+typedef struct kvq_rope_scaling {
+  kvq_rope_kind kind;
+  double factor;    /* >= 1 */
+  double original;  /* positions of the original context, > 0 (BANDS and YARN) */
+  double low, high; /* 0 <= low < high, or both 0 */
+} kvq_rope_scaling;
+KVQ_API kvq_status kvq_rope_frequencies(int32_t rotary_dim, double base, const kvq_rope_scaling *scaling,
+                                        uint64_t *freqs, float *attn_factor);
+
+/*
+ * kvq_rope -- rotary positions on queries and keys (before kvq_write_int4, say).
+ *   q, k          [T, Hq, D] and [T, Hk, D] of dtype (KVQ_BF16 / KVQ_F16 / KVQ_F32); element (t, h, d) at
+ *                 ptr + t*stride_t + h*stride_h + d. q may be NULL with Hq == 0, k with Hk == 0.
+ *   q_out, k_out  the same shapes with strides of their own; may be q and k themselves with the same
+ *                 strides. Other overlaps are not allowed.
+ *   D             1 .. 1024; any strides. Rows of 16-byte chunks whose pairs keep to chunks (D and all strides
+ *                 multiples of 8, rotary_dim of 16 or, interleaved, 8) are moved 16 bytes at a time.
+ */
+KVQ_API kvq_status kvq_rope(const void *q, int64_t q_stride_t, int64_t q_stride_h, void *q_out,
+                            int64_t qo_stride_t, int64_t qo_stride_h, int32_t Hq, const void *k,
+                            int64_t k_stride_t, int64_t k_stride_h, void *k_out, int64_t ko_stride_t,
+                            int64_t ko_stride_h, int32_t Hk, const kvq_rotary *rotary, kvq_dtype dtype,
+                            int32_t T, int32_t D, kvq_stream_t stream);
+
+/*
+ * kvq_paged_kv -- a paged cache of keys and values in 16 bits or FP8 E4M3FN.
+ *   k, v       element (block, row, head, d) at ptr + block*stride_block + row*stride_token +
+ *              head*stride_head + d: [num_blocks, block_size, Hk, D], K and V in one pool, or the head
+ *              before the token, as the strides say. Base 16-byte aligned; strides >= 0 and multiples of 16 bytes.
+ *   k_scale, v_scale  fp32 [Hk] each or NULL (1): an FP8 code c of head h stands for c * scale[h].
+ *              NULL for 16-bit caches.
+ *   dtype      KVQ_BF16, KVQ_F16 or KVQ_E4M3.
+ */
+typedef struct kvq_paged_kv {
+  void *k;
+  void *v;
+  int64_t k_stride_block, k_stride_token, k_stride_head;
+  int64_t v_stride_block, v_stride_token, v_stride_head;
+  const float *k_scale;
+  const float *v_scale;
+  kvq_dtype dtype;
+  int32_t block_size;
+  int64_t num_blocks;
+} kvq_paged_kv;
+
+/*
+ * kvq_write_kv -- write new keys and values into a kvq_paged_kv, with the rotary positions of keys and
+ * queries in the same pass.
+ *   k' = rotary(key) (key itself when rotary == NULL);  k'[t] and value[t] -> slot_mapping[t];
+ *   q_out = rotary(q)
+ * 16-bit caches hold the fp32 result rounded once; FP8 caches e4m3(clamp(x / scale[h], -448, 448)), rounded
+ * to nearest even once from fp32 (a NaN stays a NaN).
+ *
+ *   key, value    [T, Hk, D] of dtype (KVQ_BF16 or KVQ_F16; a 16-bit cache has the same type), strides as
+ *                 kvq_write_int4: base 16-byte aligned, strides multiples of 8 elements.
+ *   slot_mapping  int64 [T]; entries < 0 are skipped, entries >= num_blocks*block_size skipped and flagged (4).
+ *   q, q_out      as kvq_rope, same alignment rules as key; NULL with Hq == 0. Needs rotary.
+ *   D             a multiple of 8, at most 256. block_size >= 1.
+ */
+KVQ_API kvq_status kvq_write_kv(const void *key, int64_t k_stride_t, int64_t k_stride_h, const void *value,
+                                int64_t v_stride_t, int64_t v_stride_h, const kvq_paged_kv *cache,
+                                const int64_t *slot_mapping, const void *q, int64_t q_stride_t,
+                                int64_t q_stride_h, void *q_out, int64_t qo_stride_t, int64_t qo_stride_h,
+                                int32_t Hq, const kvq_rotary *rotary, kvq_dtype dtype, int32_t T, int32_t Hk,
+                                int32_t D, kvq_stream_t stream);
+
+/*
+ * kvq_decode_kv -- paged decode attention of one query token per sequence over a kvq_paged_kv, with the
+ * score modifiers of kvq_decode_int4_mods in the same order. With L = seq_lens[b], the query at L - 1:
+ *   S_n = softmax_scale * k_scale * q . k_n;  softcap;  window;  ALiBi     (as kvq_score_mods)
+ *   out[b][hq] = v_scale * sum_n e^{S_n} v_n / (e^{sinks[hq]} + sum_n e^{S_n})
+ * Rows with seq_lens[b] == 0 are zeros (lse: -inf, or the sink).
+ *
+ *   q             [B, Hq, D] of q_dtype (KVQ_BF16 / KVQ_F16; a 16-bit cache has the same type), contiguous,
+ *                 16-byte aligned.
+ *   block_table   int32 [B, max_blocks]; entries at or past ceil(seq_lens[b] / block_size) are not read. A block
+ *                 outside [0, num_blocks) is skipped (its keys take no part) and raises flag 1.
+ *   seq_lens      int32 [B]; clamped to [0, max_blocks * block_size] (a clamp raises flag 2).
+ *   num_splits    as kvq_decode_int4 (0: the batch's tokens balanced over the GPU).
+ *   workspace     >= kvq_decode_kv_workspace_bytes(B, Hq, Hk, D, num_splits) bytes, 16-byte aligned; no
+ *                 initialisation; calls that share one must be ordered on one stream.
+ *   out           [B, Hq, D] of out_dtype (KVQ_BF16 / KVQ_F16 / KVQ_F32), contiguous, 16-byte aligned.
+ *   mods          NULL or as kvq_decode_int4_mods; single-token only (q_len > 1 or query_start_loc:
+ *                 KVQ_ERR_UNSUPPORTED).
+ *   Supported: D in {64, 128, 256}; block_size a multiple of 16; any Hk, any Hq / Hk.
+ * Contents of the cache behind a sequence's end, and of blocks no table names, may be anything (NaN included).
+ */
+KVQ_API size_t kvq_decode_kv_workspace_bytes(int32_t B, int32_t Hq, int32_t Hk, int32_t D, int32_t num_splits);
+
+KVQ_API kvq_status kvq_decode_kv(const void *q, kvq_dtype q_dtype, const kvq_paged_kv *cache,
+                                 const int32_t *block_table, int32_t max_blocks, const int32_t *seq_lens,
+                                 float softmax_scale, int32_t num_splits, void *workspace,
+                                 size_t workspace_bytes, void *out, kvq_dtype out_dtype, int32_t B,
+                                 int32_t Hq, int32_t Hk, int32_t D, const kvq_score_mods *mods,
+                                 kvq_stream_t stream);
+
+/*
  * kvq_copy_async -- copy `bytes` bytes from src to dst with a kernel: the SMs' 16-byte loads and
  * stores (plumbing for a serving step; no counterpart on the pages). Either pointer may be device
  * memory or pinned host memory mapped into the device's address space (cudaHostAlloc /
@@ -431,6 +603,7 @@ KVQ_API kvq_status kvq_debug_set_wait(uint64_t wait_limit_ns, int32_t withhold_s
  *   16 a decode input outside the supported range: a query element beyond ~2^100 in magnitude
  *      (q, or q_rot for MSE keys, or a centroid), or a softmax weight beyond fp32 (value scales
  *      near fp32's maximum); the rows concerned may hold inf/NaN
+ *   32 the free list of kvq_plan_step ran out
  * Returns KVQ_OK when no flag was set, KVQ_ERR_OUT_OF_RANGE otherwise, KVQ_ERR_CUDA if the
  * synchronization or the read failed.
  */

@@ -202,6 +202,19 @@ void workspace_carve(void *workspace, int B, int Hq, int D, const SplitPlan &pla
   *seg_last = reinterpret_cast<int32_t *>(ws);
 }
 
+kvq_status check_paged_kv(const kvq_paged_kv *c, kvq_dtype dtype) {
+  if (c->dtype != KVQ_BF16 && c->dtype != KVQ_F16 && c->dtype != KVQ_E4M3) return KVQ_ERR_INVALID_ARG;
+  if (c->dtype != KVQ_E4M3 && (c->dtype != dtype || c->k_scale || c->v_scale)) return KVQ_ERR_INVALID_ARG;
+  if (c->block_size < 1 || c->num_blocks < 1 || !c->k || !c->v || !aligned(c->k, 16) || !aligned(c->v, 16) ||
+      !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))
+    return KVQ_ERR_INVALID_ARG;
+  const int64_t unit = c->dtype == KVQ_E4M3 ? 16 : 8;
+  for (int64_t st : {c->k_stride_block, c->k_stride_token, c->k_stride_head, c->v_stride_block, c->v_stride_token,
+                     c->v_stride_head})
+    if (st < 0 || st % unit) return KVQ_ERR_INVALID_ARG;
+  return KVQ_OK;
+}
+
 // kvq_copy_async: a grid-stride loop of 16-byte copies.
 __global__ void __launch_bounds__(256) copy16_kernel(uint4 *__restrict__ dst, const uint4 *__restrict__ src,
                                                      long long n) {
@@ -285,13 +298,15 @@ extern "C" size_t kvq_decode_workspace_bytes(int32_t B, int32_t Hq, int32_t Hk, 
 
 extern "C" kvq_status kvq_device_error(kvq_stream_t stream, uint32_t *flags) {
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  unsigned words[5] = {0, 0, 0, 0, 0};
+  unsigned words[8] = {0, 0, 0, 0, 0, 0, 0, 0};
   if (!take_flags_write(s, &words[0]) || !take_flags_decode_int4(s, &words[1]) ||
       !take_flags_decode_tq(s, &words[2]) || !take_flags_decode_tq_mse(s, &words[3]) ||
-      !take_flags_kpool(s, &words[4]))
+      !take_flags_kpool(s, &words[4]) || !take_flags_plan_step(s, &words[5]) || !take_flags_write_kv(s, &words[6]) ||
+      !take_flags_decode_kv(s, &words[7]))
     return KVQ_ERR_CUDA;
   if (cudaStreamSynchronize(s) != cudaSuccess) return KVQ_ERR_CUDA;
-  const uint32_t all = words[0] | words[1] | words[2] | words[3] | words[4];
+  uint32_t all = 0;
+  for (unsigned w : words) all |= w;
   if (flags) *flags = all;
   return all ? KVQ_ERR_OUT_OF_RANGE : KVQ_OK;
 }

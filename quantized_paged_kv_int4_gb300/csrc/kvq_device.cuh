@@ -16,7 +16,7 @@ constexpr unsigned FULL = 0xffffffffu;
 constexpr int kPage = 16;  // tokens per page: one MMA M-tile of the read kernels
 
 // Device-side error flags (kvq_device_error).
-enum : unsigned { ERR_BLOCK = 1u, ERR_SEQLEN = 2u, ERR_SLOT = 4u, ERR_TIMEOUT = 8u, ERR_RANGE = 16u };
+enum : unsigned { ERR_BLOCK = 1u, ERR_SEQLEN = 2u, ERR_SLOT = 4u, ERR_TIMEOUT = 8u, ERR_RANGE = 16u, ERR_FREE = 32u };
 
 // 2^k for an integer k in [-126, 127], exact.
 __device__ __forceinline__ float pow2i(int k) { return __int_as_float((k + 127) << 23); }

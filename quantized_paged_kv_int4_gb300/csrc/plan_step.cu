@@ -1,0 +1,289 @@
+// kvq_plan_step: the block tables and slot maps of one serving step, from the requests' lengths.
+//
+// Mathematics: three exclusive sums over the requests -- new tokens (query_start_loc), new blocks
+// (the place in the free list) and table entries (the place in the flat list of entries) -- and then
+// independent work for each table entry and each token, found by a binary search in the sums. A
+// token's block is computed from the sums too, never read back from the table this call extends, so
+// no part of the work waits for another.
+//
+// What bounds it: latency. A step's data is a few KB (32 single tokens) to ~1 MB (256 requests of 8192
+// tokens), against a launch of a few microseconds. So every CTA sums the lengths again (B words from
+// L2, one pass; at most 8192) instead of waiting for a kernel that does it once, and the whole call is
+// one launch. The only order between CTAs that exists is the cursor advanced in place: every CTA
+// reads it and one changes it. A call whose entries and tokens fit one CTA's few rounds does it behind
+// a barrier; a larger one leaves it to a second, one-CTA kernel.
+
+#include "kvq_device.cuh"
+#include "kvq_host.h"
+
+namespace kvq {
+
+__device__ unsigned g_flags_plan_step = 0;
+
+constexpr int kPlanThreads = 256;
+constexpr int kPlanMaxB = 8192;
+
+struct PlanArgs {
+  const int32_t *context, *query, *rows;
+  int32_t *table;
+  int32_t max_blocks;
+  long long num_rows;
+  const int32_t *free_blocks;
+  long long num_free;
+  const int64_t *cursor;
+  int64_t *cursor_out;
+  int32_t *seq_lens, *starts, *positions;
+  int64_t *slots;
+  int32_t *batch;
+  int32_t B, T, bs;
+  long long num_blocks;
+  int32_t advance;  // this launch writes cursor_out
+};
+
+// One request's lengths, clamped: ctx and L within the table's row, n >= 0, blocks held and needed.
+struct Request {
+  long long ctx, n, L;
+  int have, need, row;
+};
+__device__ __forceinline__ Request load_request(const PlanArgs &a, int b, unsigned *flags) {
+  Request r;
+  const long long cap = static_cast<long long>(a.max_blocks) * a.bs;
+  const long long c = __ldg(a.context + b), q = a.query != nullptr ? __ldg(a.query + b) : 1;
+  r.row = a.rows != nullptr ? __ldg(a.rows + b) : b;
+  r.n = q < 0 ? 0 : q;
+  r.ctx = c < 0 ? 0 : (c > cap ? cap : c);
+  const long long L = (c < 0 ? 0 : c) + r.n;
+  r.L = L > cap ? cap : L;
+  if (flags != nullptr && (c < 0 || q < 0 || L > cap)) atomicOr(flags, ERR_SEQLEN);
+  if (r.row < 0 || r.row >= a.num_rows) {
+    if (flags != nullptr) atomicOr(flags, ERR_BLOCK);
+    r.row = -1;
+    r.have = r.need = 0;
+  } else {
+    r.need = (static_cast<unsigned>(r.L) + a.bs - 1) / static_cast<unsigned>(a.bs);  // L <= cap <= 2^31 - 1
+    r.have = a.free_blocks != nullptr ? (static_cast<unsigned>(r.ctx) + a.bs - 1) / static_cast<unsigned>(a.bs) : r.need;
+  }
+  return r;
+}
+
+// The id of block j of a request; off: its place in the free list is off + j - have.
+__device__ __forceinline__ int block_id(const PlanArgs &a, const Request &r, int j, long long off, unsigned *flags) {
+  if (j < r.have) return a.table[static_cast<long long>(r.row) * a.max_blocks + j];
+  const long long i = off + j - r.have;
+  if (i >= a.num_free || i < 0) {
+    atomicOr(flags, ERR_FREE);
+    return -1;
+  }
+  const int id = __ldg(a.free_blocks + i);
+  if (id < 0 || id >= a.num_blocks) {
+    atomicOr(flags, ERR_BLOCK);
+    return -1;
+  }
+  return id;
+}
+
+// Largest b in [0, B) with first[b] <= i, given first[0] <= i < first[B] (requests of no length skipped).
+__device__ __forceinline__ int find_request(const long long *first, int B, long long i) {
+  int lo = 0, hi = B;  // first[lo] <= i < first[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (first[mid] <= i) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+extern __shared__ __align__(16) long long kvq_plan_smem[];
+
+__global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanArgs a) {
+  long long *tok = kvq_plan_smem, *ent = tok + a.B + 1;  // exclusive sums [B + 1] each
+  int32_t *blk = reinterpret_cast<int32_t *>(ent + a.B + 1);
+  __shared__ long long s_warp[3][kPlanThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  unsigned *report = blockIdx.x == 0 ? &g_flags_plan_step : nullptr;  // each fault once
+
+  // a run of requests for each thread, their sums scanned over the block
+  const int per = (a.B + kPlanThreads - 1) / kPlanThreads, b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
+  long long sum[3] = {0, 0, 0};  // tokens, entries, new blocks
+  for (int b = b0; b < b1; ++b) {
+    const Request r = load_request(a, b, report);
+    sum[0] += r.n;
+    sum[1] += a.batch != nullptr ? r.need : r.need - r.have;
+    sum[2] += r.need - r.have;
+  }
+  long long own[3], total[3];
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    own[k] = sum[k];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(FULL, sum[k], o);
+      if (lane >= o) sum[k] += v;
+    }
+    if (lane == 31) s_warp[k][warp] = sum[k];
+  }
+  const long long cursor = a.cursor != nullptr ? *a.cursor : 0;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    long long before = 0;
+    total[k] = 0;
+#pragma unroll
+    for (int w = 0; w < kPlanThreads / 32; ++w) {
+      before += w < warp ? s_warp[k][w] : 0;
+      total[k] += s_warp[k][w];
+    }
+    sum[k] += before - own[k];  // exclusive
+  }
+  for (int b = b0; b < b1; ++b) {
+    const Request r = load_request(a, b, nullptr);
+    tok[b] = sum[0];
+    ent[b] = sum[1];
+    blk[b] = static_cast<int32_t>(sum[2] < 0x7fffffffLL ? sum[2] : 0x7fffffffLL);
+    if (blockIdx.x == 0) {
+      if (a.seq_lens != nullptr) a.seq_lens[b] = static_cast<int32_t>(r.L);
+      if (a.starts != nullptr) a.starts[b] = static_cast<int32_t>(min(sum[0], 0x7fffffffLL));
+    }
+    sum[0] += r.n;
+    sum[1] += a.batch != nullptr ? r.need : r.need - r.have;
+    sum[2] += r.need - r.have;
+  }
+  if (tid == 0) {
+    tok[a.B] = total[0];
+    ent[a.B] = total[1];
+    if (blockIdx.x == 0) {
+      if (a.starts != nullptr) a.starts[a.B] = static_cast<int32_t>(min(total[0], 0x7fffffffLL));
+      if (total[0] > a.T && (a.positions != nullptr || a.slots != nullptr)) atomicOr(&g_flags_plan_step, ERR_SEQLEN);
+    }
+  }
+  __syncthreads();
+  if (a.advance && blockIdx.x == 0 && tid == 0) {  // one CTA, or a cursor_out of its own
+    const long long c = cursor + total[2], end = max(static_cast<long long>(a.num_free), cursor);
+    *a.cursor_out = min(c, end);
+  }
+
+  const long long stride = static_cast<long long>(gridDim.x) * kPlanThreads;
+  const long long first = static_cast<long long>(blockIdx.x) * kPlanThreads + tid;
+  for (long long i = first; i < total[1]; i += stride) {
+    const int b = find_request(ent, a.B, i);
+    const Request r = load_request(a, b, nullptr);
+    const int j = static_cast<int>(i - ent[b]) + (a.batch != nullptr ? 0 : r.have);
+    const int id = block_id(a, r, j, cursor + blk[b], &g_flags_plan_step);
+    if (j >= r.have) a.table[static_cast<long long>(r.row) * a.max_blocks + j] = id;
+    if (a.batch != nullptr) a.batch[static_cast<long long>(b) * a.max_blocks + j] = id;
+  }
+  if (a.positions == nullptr && a.slots == nullptr) return;
+  for (long long i = first; i < a.T; i += stride) {
+    long long p = -1, slot = -1;
+    if (i < total[0]) {
+      const int b = find_request(tok, a.B, i);
+      const Request r = load_request(a, b, nullptr);
+      p = r.ctx + (i - tok[b]);
+      if (p < r.L && r.row >= 0) {
+        const int pos = static_cast<int>(p), j = pos / a.bs;  // p < L <= 2^31 - 1
+        const int id = block_id(a, r, j, cursor + blk[b], &g_flags_plan_step);
+        if (id >= 0 && id < a.num_blocks)
+          slot = static_cast<long long>(id) * a.bs + (pos - j * a.bs);
+        else if (j < r.have)
+          atomicOr(&g_flags_plan_step, ERR_BLOCK);
+      }
+    }
+    if (a.positions != nullptr) a.positions[i] = static_cast<int32_t>(min(p, 0x7fffffffLL));
+    if (a.slots != nullptr) a.slots[i] = slot;
+  }
+}
+
+// cursor advanced in place, behind the kernel that read it
+__global__ void __launch_bounds__(kPlanThreads) plan_advance_kernel(const PlanArgs a) {
+  __shared__ long long s_warp[kPlanThreads / 32];
+  long long n = 0;
+  for (int b = threadIdx.x; b < a.B; b += kPlanThreads) {
+    const Request r = load_request(a, b, nullptr);
+    n += r.need - r.have;
+  }
+#pragma unroll
+  for (int m = 16; m >= 1; m >>= 1) n += __shfl_xor_sync(FULL, n, m);
+  if ((threadIdx.x & 31) == 0) s_warp[threadIdx.x >> 5] = n;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    n = 0;
+    for (int w = 0; w < kPlanThreads / 32; ++w) n += s_warp[w];
+    const long long c = *a.cursor, end = max(a.num_free, c);
+    *a.cursor_out = min(c + n, end);
+  }
+}
+
+bool take_flags_plan_step(cudaStream_t stream, unsigned *host_word) {
+  static const unsigned zero = 0;
+  if (cudaMemcpyFromSymbolAsync(host_word, g_flags_plan_step, sizeof(unsigned), 0, cudaMemcpyDeviceToHost, stream) !=
+      cudaSuccess)
+    return false;
+  return cudaMemcpyToSymbolAsync(g_flags_plan_step, &zero, sizeof(unsigned), 0, cudaMemcpyHostToDevice, stream) ==
+         cudaSuccess;
+}
+
+}  // namespace kvq
+
+using namespace kvq;
+
+extern "C" kvq_status kvq_plan_step(const int32_t *context_lens, const int32_t *query_lens, const int32_t *rows,
+                                    int32_t *block_table, int32_t max_blocks, int64_t num_rows,
+                                    const int32_t *free_blocks, int64_t num_free, const int64_t *cursor,
+                                    int64_t *cursor_out, int32_t *seq_lens, int32_t *query_start_loc,
+                                    int32_t *positions, int64_t *slot_mapping, int32_t *batch_table, int32_t B,
+                                    int32_t T, int32_t block_size, int64_t num_blocks, kvq_stream_t stream) {
+  if (B < 0 || T < 0 || max_blocks < 0 || num_rows < 0 || num_free < 0 || block_size < 1 || num_blocks < 1)
+    return KVQ_ERR_INVALID_ARG;
+  if (B > kPlanMaxB) return KVQ_ERR_UNSUPPORTED;
+  if (static_cast<long long>(max_blocks) * block_size > 0x7fffffffLL) return KVQ_ERR_UNSUPPORTED;  // int32 lengths
+  if ((free_blocks == nullptr) != (cursor == nullptr) || (free_blocks == nullptr) != (cursor_out == nullptr))
+    return KVQ_ERR_INVALID_ARG;
+  if (B > 0 && (!context_lens || !block_table || max_blocks < 1 || num_rows < 1 || (!rows && num_rows < B)))
+    return KVQ_ERR_INVALID_ARG;
+  if (!aligned(context_lens, 4) || !aligned(query_lens, 4) || !aligned(rows, 4) || !aligned(block_table, 4) ||
+      !aligned(free_blocks, 4) || !aligned(cursor, 8) || !aligned(cursor_out, 8) || !aligned(seq_lens, 4) ||
+      !aligned(query_start_loc, 4) || !aligned(positions, 4) || !aligned(slot_mapping, 8) || !aligned(batch_table, 4))
+    return KVQ_ERR_INVALID_ARG;
+  if (batch_table != nullptr && batch_table == block_table) return KVQ_ERR_INVALID_ARG;
+  if (seq_lens != nullptr && (seq_lens == context_lens || seq_lens == query_lens)) return KVQ_ERR_INVALID_ARG;
+
+  PlanArgs a;
+  a.context = context_lens;
+  a.query = query_lens;
+  a.rows = rows;
+  a.table = block_table;
+  a.max_blocks = max_blocks;
+  a.num_rows = num_rows;
+  a.free_blocks = free_blocks;
+  a.num_free = num_free;
+  a.cursor = cursor;
+  a.cursor_out = cursor_out;
+  a.seq_lens = seq_lens;
+  a.starts = query_start_loc;
+  a.positions = positions;
+  a.slots = slot_mapping;
+  a.batch = batch_table;
+  a.B = B;
+  a.T = T;
+  a.bs = block_size;
+  a.num_blocks = num_blocks;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  // The entries are known on the device only; the host bounds them by the tables' width. Four rounds of a
+  // CTA cost less than the second launch that an advanced cursor would need.
+  const long long entries = batch_table != nullptr ? static_cast<long long>(B) * max_blocks : T / block_size + B;
+  const long long most = entries > T ? entries : T;
+  const bool in_place = cursor != nullptr && cursor == cursor_out;
+  long long grid = (most + kPlanThreads - 1) / kPlanThreads;
+  if (grid < 1 || (in_place && grid <= 4)) grid = 1;
+  const long long cap = 2LL * (sm_count() > 0 ? sm_count() : 1);
+  if (grid > cap) grid = cap;
+  a.advance = cursor_out != nullptr && (grid == 1 || !in_place);
+  const size_t smem = (static_cast<size_t>(B) + 1) * (2 * sizeof(long long) + sizeof(int32_t));
+  if (smem > 48 * 1024) {
+    static size_t attr_done[kMaxDevices] = {};
+    if (ensure_dynamic_smem(plan_step_kernel, smem, attr_done) != cudaSuccess) return KVQ_ERR_CUDA;
+  }
+  plan_step_kernel<<<static_cast<unsigned>(grid), kPlanThreads, smem, s>>>(a);
+  if (cudaGetLastError() != cudaSuccess) return KVQ_ERR_CUDA;
+  if (in_place && grid > 1) plan_advance_kernel<<<1, kPlanThreads, 0, s>>>(a);
+  return launch_status();
+}

@@ -20,14 +20,17 @@ KVQ_ERR_UNSUPPORTED = 2
 KVQ_ERR_WORKSPACE = 3
 KVQ_ERR_OUT_OF_RANGE = 4
 KVQ_ERR_CUDA = 5
-KVQ_BF16, KVQ_F16, KVQ_F32 = 0, 1, 2
+KVQ_BF16, KVQ_F16, KVQ_F32, KVQ_E4M3 = 0, 1, 2, 3
+ROPE_KINDS = {"none": 0, "linear": 1, "bands": 2, "yarn": 3}
 
 # the C API's declared functions, in header order
 C_FUNCTIONS = ("kvq_status_string", "kvq_abi_version", "kvq_write_int4", "kvq_decode_workspace_bytes",
                "kvq_decode_int4", "kvq_decode_int4_mods", "kvq_decode_int4_mods_workspace_bytes",
                "kvq_decode_int4_noalloc", "kvq_decode_tq",
                "kvq_decode_tq_lse", "kvq_decode_tq_mse_workspace_bytes", "kvq_decode_tq_mse", "kvq_kpool_write",
-               "kvq_kpool_seed_tail", "kvq_kpool_decode_update", "kvq_fwht128", "kvq_copy_async",
+               "kvq_kpool_seed_tail", "kvq_kpool_decode_update", "kvq_fwht128", "kvq_plan_step",
+               "kvq_rope_frequencies", "kvq_rope", "kvq_write_kv", "kvq_decode_kv_workspace_bytes",
+               "kvq_decode_kv", "kvq_copy_async",
                "kvq_debug_set_wait", "kvq_device_error")
 KVQ_NOALLOC_SCRATCH_BYTES = 16 << 20
 
@@ -41,6 +44,25 @@ class ScoreMods(ctypes.Structure):
     """kvq_score_mods (include/kvq.h)."""
     _fields_ = [("sliding_window", c_i32), ("softcap", c_f32), ("sinks", c_p), ("alibi_slopes", c_p),
                 ("q_len", c_i32), ("lse_out", c_p), ("query_start_loc", c_p), ("total_q", c_i32)]
+
+
+class Rotary(ctypes.Structure):
+    """kvq_rotary (include/kvq.h)."""
+    _fields_ = [("positions", c_p), ("freqs", c_p), ("rotary_dim", c_i32), ("interleaved", c_i32),
+                ("attn_factor", c_f32)]
+
+
+class RopeScaling(ctypes.Structure):
+    """kvq_rope_scaling (include/kvq.h)."""
+    _fields_ = [("kind", ctypes.c_int), ("factor", ctypes.c_double), ("original", ctypes.c_double),
+                ("low", ctypes.c_double), ("high", ctypes.c_double)]
+
+
+class PagedKv(ctypes.Structure):
+    """kvq_paged_kv (include/kvq.h)."""
+    _fields_ = [("k", c_p), ("v", c_p), ("k_stride_block", c_i64), ("k_stride_token", c_i64), ("k_stride_head", c_i64),
+                ("v_stride_block", c_i64), ("v_stride_token", c_i64), ("v_stride_head", c_i64), ("k_scale", c_p),
+                ("v_scale", c_p), ("dtype", ctypes.c_int), ("block_size", c_i32), ("num_blocks", c_i64)]
 
 
 _SIGS = {
@@ -72,6 +94,19 @@ _SIGS = {
                                                c_i64, c_p, c_i64, c_i64, c_p, c_p, c_p, c_i32, c_i32, c_i32, c_i32,
                                                c_i32, c_p]),
     "kvq_fwht128": (ctypes.c_int, [c_p, c_p, c_p, c_i64, c_p]),
+    "kvq_plan_step": (ctypes.c_int, [c_p, c_p, c_p, c_p, c_i32, c_i64, c_p, c_i64, c_p, c_p, c_p, c_p, c_p, c_p, c_p,
+                                     c_i32, c_i32, c_i32, c_i64, c_p]),
+    "kvq_rope_frequencies": (ctypes.c_int, [c_i32, ctypes.c_double, ctypes.POINTER(RopeScaling), c_p,
+                                            ctypes.POINTER(c_f32)]),
+    "kvq_rope": (ctypes.c_int, [c_p, c_i64, c_i64, c_p, c_i64, c_i64, c_i32, c_p, c_i64, c_i64, c_p, c_i64, c_i64,
+                                c_i32, ctypes.POINTER(Rotary), ctypes.c_int, c_i32, c_i32, c_p]),
+    "kvq_write_kv": (ctypes.c_int, [c_p, c_i64, c_i64, c_p, c_i64, c_i64, ctypes.POINTER(PagedKv), c_p, c_p, c_i64,
+                                    c_i64, c_p, c_i64, c_i64, c_i32, ctypes.POINTER(Rotary), ctypes.c_int, c_i32,
+                                    c_i32, c_i32, c_p]),
+    "kvq_decode_kv_workspace_bytes": (c_sz, [c_i32, c_i32, c_i32, c_i32, c_i32]),
+    "kvq_decode_kv": (ctypes.c_int, [c_p, ctypes.c_int, ctypes.POINTER(PagedKv), c_p, c_i32, c_p, c_f32, c_i32, c_p,
+                                     c_sz, c_p, ctypes.c_int, c_i32, c_i32, c_i32, c_i32, ctypes.POINTER(ScoreMods),
+                                     c_p]),
     "kvq_debug_set_wait": (ctypes.c_int, [ctypes.c_uint64, c_i32]),
     "kvq_device_error": (ctypes.c_int, [c_p, ctypes.POINTER(ctypes.c_uint32)]),
 }
@@ -473,6 +508,281 @@ def kvq_device_error(stream=None):
     flags = ctypes.c_uint32(0)
     st = lib().kvq_device_error(_stream(stream), ctypes.byref(flags))
     return int(st), int(flags.value)
+
+
+# ----------------------------------------------------------------------------------------------
+# A serving step over 16-bit and FP8 paged caches: block tables and slot maps, rotary positions, the
+# cache write and the split decode.
+# ----------------------------------------------------------------------------------------------
+_CACHE_CODES = {torch.bfloat16: KVQ_BF16, torch.float16: KVQ_F16, torch.float8_e4m3fn: KVQ_E4M3}
+
+
+def _same_device(ref, tensors):
+    for t, n in tensors:
+        if t is not None and t.device != ref.device:
+            raise ValueError("%s is on %s, the call on %s" % (n, t.device, ref.device))
+
+
+def _call(fn, where, device, stream, *args):
+    """fn(*args, stream) with the tensors' device current and, by default, that device's current stream."""
+    if device.index == torch.cuda.current_device():
+        _check(fn(*args, _stream(stream)), where)
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, _stream(stream)), where)
+
+
+def _rows(t, name, dtype, shape):
+    """A CUDA tensor [T, heads, D] of a type and shape (None: any) with a contiguous last dim."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("%s must be a CUDA tensor" % name)
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] > 1) or (shape is not None and tuple(t.shape) != shape):
+        raise ValueError("%s must be %s with a contiguous last dim, got %s" % (name, shape or "[T, heads, D]", tuple(t.shape)))
+
+
+def _rotary(positions, freqs, interleaved, attn_factor, T, D):
+    _need(positions, "positions", torch.int32)
+    _need(freqs, "freqs", torch.int64)
+    if positions.numel() != T:
+        raise ValueError("positions must have T = %d entries" % T)
+    if freqs.dim() != 1 or not 1 <= freqs.numel() <= D // 2:
+        raise ValueError("freqs must be [rotary_dim / 2] with rotary_dim <= D = %d" % D)
+    return Rotary(positions.data_ptr(), freqs.data_ptr(), 2 * freqs.numel(), 1 if interleaved else 0, float(attn_factor))
+
+
+def _paged_kv(k_cache, v_cache, k_scale, v_scale):
+    """The PagedKv of two [num_blocks, block_size, Hk, D] views (any strides, last dim contiguous)."""
+    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError("%s must be a CUDA tensor" % n)
+        if t.dtype not in _CACHE_CODES or t.dtype != k_cache.dtype:
+            raise TypeError("k_cache / v_cache must both be bfloat16, float16 or float8_e4m3fn")
+        if t.dim() != 4 or t.stride(3) != 1 or t.shape != k_cache.shape:
+            raise ValueError("k_cache / v_cache must both be [num_blocks, block_size, Hk, D] with a contiguous last dim")
+    nb, bs, Hk, _ = k_cache.shape
+    for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        if t is not None:
+            _need(t, n, torch.float32)
+            if t.numel() != Hk:
+                raise ValueError("%s must have Hk = %d entries" % (n, Hk))
+    _same_device(k_cache, ((v_cache, "v_cache"), (k_scale, "k_scale"), (v_scale, "v_scale")))
+    ks, vs = k_cache.stride(), v_cache.stride()
+    return PagedKv(k_cache.data_ptr(), v_cache.data_ptr(), ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], _ptr(k_scale),
+                   _ptr(v_scale), _CACHE_CODES[k_cache.dtype], bs, nb)
+
+
+def kvq_plan_step(context_lens, query_lens, block_table, free_blocks, cursor, block_size, num_blocks, rows=None,
+                  batch_table=None, cursor_out=None, seq_lens=None, query_start_loc=None, positions=None,
+                  slot_mapping=None, T=None, stream=None):
+    """The block tables and slot maps of one step from the requests' lengths (include/kvq.h).
+
+    context_lens / query_lens int32 [B] (query_lens None: one new token each); block_table int32
+    [rows, max_blocks], extended in place from free_blocks (int32) and cursor (int64 [1], advanced in
+    place or into cursor_out; both None: the table already holds every block); rows int32 [B]: the
+    requests' rows. Outputs that are not given are allocated (batch_table only when given; T rows of
+    positions and slot_mapping: required then unless one of them is given).
+    Returns (seq_lens, query_start_loc, positions, slot_mapping)."""
+    _need(context_lens, "context_lens", torch.int32)
+    _need(block_table, "block_table", torch.int32)
+    B = context_lens.numel()
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [rows, max_blocks]")
+    for t, n in ((query_lens, "query_lens"), (rows, "rows"), (free_blocks, "free_blocks"), (batch_table, "batch_table"),
+                 (seq_lens, "seq_lens"), (query_start_loc, "query_start_loc"), (positions, "positions")):
+        if t is not None:
+            _need(t, n, torch.int32)
+    for t, n in ((cursor, "cursor"), (cursor_out, "cursor_out"), (slot_mapping, "slot_mapping")):
+        if t is not None:
+            _need(t, n, torch.int64)
+    if (free_blocks is None) != (cursor is None):
+        raise ValueError("free_blocks and cursor go together")
+    if cursor_out is None:
+        cursor_out = cursor
+    for t, n, size in ((query_lens, "query_lens", B), (rows, "rows", B), (seq_lens, "seq_lens", B),
+                       (query_start_loc, "query_start_loc", B + 1), (cursor, "cursor", 1), (cursor_out, "cursor_out", 1)):
+        if t is not None and t.numel() != size:
+            raise ValueError("%s must have %d entries, got %d" % (n, size, t.numel()))
+    if batch_table is not None and tuple(batch_table.shape) != (B, block_table.shape[1]):
+        raise ValueError("batch_table must be [B, max_blocks] = %s" % ((B, block_table.shape[1]),))
+    if T is None:
+        given = positions if positions is not None else slot_mapping
+        if given is None:
+            raise ValueError("T, the rows of positions and slot_mapping, is needed")
+        T = given.numel()
+    for t, n in ((positions, "positions"), (slot_mapping, "slot_mapping")):
+        if t is not None and t.numel() != T:
+            raise ValueError("%s must have T = %d entries" % (n, T))
+    dev = context_lens.device
+    if seq_lens is None:
+        seq_lens = torch.empty(B, dtype=torch.int32, device=dev)
+    if query_start_loc is None:
+        query_start_loc = torch.empty(B + 1, dtype=torch.int32, device=dev)
+    if positions is None:
+        positions = torch.empty(T, dtype=torch.int32, device=dev)
+    if slot_mapping is None:
+        slot_mapping = torch.empty(T, dtype=torch.int64, device=dev)
+    _same_device(context_lens, ((query_lens, "query_lens"), (block_table, "block_table"), (rows, "rows"),
+                                (free_blocks, "free_blocks"), (cursor, "cursor"), (cursor_out, "cursor_out"),
+                                (batch_table, "batch_table"), (seq_lens, "seq_lens"), (positions, "positions"),
+                                (query_start_loc, "query_start_loc"), (slot_mapping, "slot_mapping")))
+    _call(lib().kvq_plan_step, "kvq_plan_step", dev, stream, _ptr(context_lens), _ptr(query_lens), _ptr(rows),
+          _ptr(block_table), block_table.shape[1], block_table.shape[0], _ptr(free_blocks),
+          0 if free_blocks is None else free_blocks.numel(), _ptr(cursor), _ptr(cursor_out), _ptr(seq_lens),
+          _ptr(query_start_loc), _ptr(positions), _ptr(slot_mapping), _ptr(batch_table), B, T, int(block_size),
+          int(num_blocks))
+    return seq_lens, query_start_loc, positions, slot_mapping
+
+
+def kvq_rope_frequencies(rotary_dim, base=10000.0, scaling="none", factor=1.0, original=0.0, low=0.0, high=0.0,
+                         device=None):
+    """(freqs int64 [rotary_dim / 2], attn_factor) of kvq_rope and kvq_write_kv: the pairs' phase advance a position
+    in units of 2^-64 turns. scaling: "none", "linear", "bands" or "yarn" (kvq_rope_scaling in include/kvq.h)."""
+    if scaling not in ROPE_KINDS:
+        raise ValueError("scaling must be one of %s" % ", ".join(ROPE_KINDS))
+    freqs = torch.empty(max(int(rotary_dim) // 2, 1), dtype=torch.int64)
+    attn = c_f32(0.0)
+    sc = RopeScaling(ROPE_KINDS[scaling], float(factor), float(original), float(low), float(high))
+    _check(lib().kvq_rope_frequencies(int(rotary_dim), float(base), ctypes.byref(sc), freqs.data_ptr(),
+                                      ctypes.byref(attn)), "kvq_rope_frequencies")
+    return freqs.to(device) if device is not None else freqs, float(attn.value)
+
+
+def kvq_rope(q, k, positions, freqs, interleaved=False, attn_factor=1.0, q_out=None, k_out=None, stream=None):
+    """Rotary positions: q [T, Hq, D] and k [T, Hk, D] (bf16 / f16 / f32, last dim contiguous; either may be None) ->
+    (q_out, k_out), new contiguous tensors by default; pass q_out=q, k_out=k for in place. Rows whose position is
+    negative are padding and stay unwritten."""
+    ref = q if q is not None else k
+    if not isinstance(ref, torch.Tensor) or ref.dim() != 3:
+        raise TypeError("q or k must be a CUDA tensor [T, heads, D]")
+    T, _, D = ref.shape
+    if ref.dtype not in _OUT_CODES:
+        raise TypeError("q / k must be bfloat16, float16 or float32, got %s" % ref.dtype)
+    rows = []
+    for x, out, n in ((q, q_out, "q"), (k, k_out, "k")):
+        if x is None:
+            rows.append((None, 0, 0, None, 0, 0, 0))
+            if out is not None:
+                raise ValueError("%s_out without %s" % (n, n))
+            continue
+        _rows(x, n, ref.dtype, (T, x.shape[1], D) if x.dim() == 3 else (T, "heads", D))
+        if out is None:
+            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        _rows(out, n + "_out", x.dtype, tuple(x.shape))
+        _same_device(ref, ((x, n), (out, n + "_out")))
+        if n == "q":
+            q_out = out
+        else:
+            k_out = out
+        rows.append((x.data_ptr(), x.stride(0), x.stride(1), out.data_ptr(), out.stride(0), out.stride(1), x.shape[1]))
+    rot = _rotary(positions, freqs, interleaved, attn_factor, T, D)
+    _same_device(ref, ((positions, "positions"), (freqs, "freqs")))
+    _call(lib().kvq_rope, "kvq_rope", ref.device, stream, *rows[0], *rows[1], ctypes.byref(rot), _OUT_CODES[ref.dtype],
+          T, D)
+    return q_out, k_out
+
+
+def kvq_write_kv(key, value, k_cache, v_cache, slot_mapping, k_scale=None, v_scale=None, q=None, positions=None,
+                 freqs=None, interleaved=False, attn_factor=1.0, q_out=None, stream=None):
+    """Write key / value [T, Hk, D] (bf16 / f16) at slot_mapping (int64 [T]) of a paged cache: k_cache / v_cache
+    [num_blocks, block_size, Hk, D] views of the same type or float8_e4m3fn (codes of x / scale[head]).
+    With positions (int32 [T]) and freqs (kvq_rope_frequencies) the keys are rotated on the way, and q
+    [T, Hq, D] into q_out. Returns q_out (None without q)."""
+    if not isinstance(key, torch.Tensor) or key.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError("key must be a CUDA bfloat16 or float16 tensor")
+    _rows(key, "key", key.dtype, None)
+    _rows(value, "value", key.dtype, tuple(key.shape))
+    T, Hk, D = key.shape
+    kv = _paged_kv(k_cache, v_cache, k_scale, v_scale)
+    if k_cache.shape[2] != Hk or k_cache.shape[3] != D:
+        raise ValueError("cache shapes do not match key")
+    if k_cache.dtype != torch.float8_e4m3fn and (k_cache.dtype != key.dtype or k_scale is not None or v_scale is not None):
+        raise TypeError("a 16-bit cache has key's type and no scales")
+    _need(slot_mapping, "slot_mapping", torch.int64)
+    if slot_mapping.numel() != T:
+        raise ValueError("slot_mapping must have T = %d entries" % T)
+    if (positions is None) != (freqs is None):
+        raise ValueError("positions and freqs go together")
+    rot, qrow = None, (None, 0, 0, None, 0, 0, 0)
+    if positions is not None:
+        rot = _rotary(positions, freqs, interleaved, attn_factor, T, D)
+    if q is not None:
+        if rot is None:
+            raise ValueError("q is only rotated: positions and freqs are needed")
+        _rows(q, "q", key.dtype, (T, q.shape[1], D) if q.dim() == 3 else (T, "heads", D))
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        _rows(q_out, "q_out", q.dtype, tuple(q.shape))
+        qrow = (q.data_ptr(), q.stride(0), q.stride(1), q_out.data_ptr(), q_out.stride(0), q_out.stride(1), q.shape[1])
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    _same_device(key, ((value, "value"), (k_cache, "k_cache"), (slot_mapping, "slot_mapping"), (positions, "positions"),
+                       (freqs, "freqs"), (q, "q"), (q_out, "q_out")))
+    _call(lib().kvq_write_kv, "kvq_write_kv", key.device, stream, key.data_ptr(), key.stride(0), key.stride(1),
+          value.data_ptr(), value.stride(0), value.stride(1), ctypes.byref(kv), slot_mapping.data_ptr(), *qrow,
+          None if rot is None else ctypes.byref(rot), _OUT_CODES[key.dtype], T, Hk, D)
+    return q_out
+
+
+def kvq_decode_kv_workspace_bytes(B, Hq, Hk, D, num_splits=0):
+    return int(lib().kvq_decode_kv_workspace_bytes(B, Hq, Hk, D, num_splits))
+
+
+def kvq_decode_kv(q, k_cache, v_cache, block_table, seq_lens, softmax_scale, k_scale=None, v_scale=None, out=None,
+                  workspace=None, num_splits=0, out_dtype=None, stream=None, sliding_window=0, softcap=0.0, sinks=None,
+                  alibi_slopes=None, lse_out=None):
+    """Decode attention of one token per sequence over a 16-bit or FP8 paged cache: q [B, Hq, D] (bf16 / f16),
+    k_cache / v_cache as kvq_write_kv -> out [B, Hq, D] (q's type by default). Modifiers and lse_out (fp32
+    [B, Hq]) as kvq_decode_int4. Returns out."""
+    if not isinstance(q, torch.Tensor) or q.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError("q must be a CUDA bfloat16 or float16 tensor")
+    _need(q, "q")
+    _need(block_table, "block_table", torch.int32)
+    _need(seq_lens, "seq_lens", torch.int32)
+    if q.dim() != 3:
+        raise ValueError("q must be [B, Hq, D]")
+    B, Hq, D = q.shape
+    kv = _paged_kv(k_cache, v_cache, k_scale, v_scale)
+    Hk = k_cache.shape[2]
+    if k_cache.shape[3] != D:
+        raise ValueError("the cache's head size is %d, q's %d" % (k_cache.shape[3], D))
+    if k_cache.dtype != torch.float8_e4m3fn and (k_cache.dtype != q.dtype or k_scale is not None or v_scale is not None):
+        raise TypeError("a 16-bit cache has q's type and no scales")
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table must be [B, max_blocks] with B = %d" % B)
+    if seq_lens.numel() != B:
+        raise ValueError("seq_lens must have B = %d entries" % B)
+    if out is None:
+        out = torch.empty((B, Hq, D), dtype=out_dtype or q.dtype, device=q.device)
+    _need(out, "out")
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape %s, got %s" % (tuple(q.shape), tuple(out.shape)))
+    mods = None
+    if sliding_window or softcap or sinks is not None or alibi_slopes is not None or lse_out is not None:
+        for t, n in ((sinks, "sinks"), (alibi_slopes, "alibi_slopes")):
+            if t is not None:
+                _need(t, n, torch.float32)
+                if t.numel() != Hq:
+                    raise ValueError("%s must have Hq = %d entries" % (n, Hq))
+        if lse_out is not None:
+            _need(lse_out, "lse_out", torch.float32)
+            if tuple(lse_out.shape) != (B, Hq):
+                raise ValueError("lse_out must be [%d, %d]" % (B, Hq))
+        mods = ScoreMods(int(sliding_window), float(softcap), _ptr(sinks), _ptr(alibi_slopes), 1, _ptr(lse_out), None, 0)
+    if workspace is None:
+        need = kvq_decode_kv_workspace_bytes(B, Hq, Hk, D, num_splits) if Hk else 0
+        workspace = torch.empty((max(need, 16),), dtype=torch.uint8, device=q.device)
+        if stream is not None:  # freed here, in use there until the call's kernels end
+            workspace.record_stream(stream)
+    _need(workspace, "workspace", torch.uint8)
+    _same_device(q, ((k_cache, "k_cache"), (block_table, "block_table"), (seq_lens, "seq_lens"), (out, "out"),
+                     (workspace, "workspace"), (sinks, "sinks"), (alibi_slopes, "alibi_slopes"), (lse_out, "lse_out")))
+    _call(lib().kvq_decode_kv, "kvq_decode_kv", q.device, stream, q.data_ptr(), _OUT_CODES[q.dtype], ctypes.byref(kv),
+          block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(), float(softmax_scale), int(num_splits),
+          workspace.data_ptr(), workspace.numel(), out.data_ptr(), _out_code(out.dtype), B, Hq, Hk, D,
+          None if mods is None else ctypes.byref(mods))
+    return out
 
 
 # ----------------------------------------------------------------------------------------------

@@ -1,0 +1,295 @@
+"""kvq_decode_kv against the float64 oracle on the values the cache holds.
+
+Bound of an output element o = sum p v, with A = sum p |v| (weights p that sum to at most 1):
+  the weights enter the product with a relative error of 2^-11 (fp16; fp16 and FP8 caches) or 2^-16 (bf16 in two
+  parts); scores are sums of D exact products in fp32 and lie below 2^5 here, an error below 2^-14; the exponential,
+  the sums over a few hundred tiles and the joining add less than 2^-13: (w + 2^-12) A in all; and half a step of the
+  output's type, eps / 2 |o|.
+Bound of the log-sum-exp: the scores' error and fp32 roundings of a value below 2^5: 1e-4."""
+
+import itertools
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import paged_kv
+from quantized_paged_kv_int4_gb300 import kvq
+
+pytestmark = pytest.mark.gpu
+
+BF, F16, F32, E4 = torch.bfloat16, torch.float16, torch.float32, torch.float8_e4m3fn
+
+
+def f64(x):
+    return x.detach().float().cpu().double().numpy()
+
+
+class Case:
+    """Seeded q, pools whose unused rows and blocks hold NaN, and the oracle's view of the same values."""
+
+    def __init__(self, lens, Hq, Hk, D, cache=BF, q_dtype=None, bs=16, layout="apart", seed=0, spare=3, q_mul=1.0):
+        g = torch.Generator().manual_seed(seed)
+        B = len(lens)
+        q_dtype = q_dtype or (BF if cache == E4 else cache)
+        pages = [-(-n // bs) for n in lens]
+        nb = sum(pages) + spare
+        ids = torch.randperm(nb, generator=g).tolist()
+        table = torch.full((B, max(pages + [1]) + 1), -9, dtype=torch.int32)  # unused entries: no block at all
+        k, v = (torch.full((nb, bs, Hk, D), float("nan")) for _ in range(2))
+        at = 0
+        for b, n in enumerate(lens):
+            mine = ids[at:at + pages[b]]
+            at += pages[b]
+            table[b, :pages[b]] = torch.tensor(mine, dtype=torch.int32)
+            for x in (k, v):
+                rows = torch.randn((n, Hk, D), generator=g)
+                pos = torch.arange(n)
+                x[torch.tensor(mine, dtype=torch.int64)[pos // bs] if n else pos, pos % bs] = rows
+        self.k_scale = self.v_scale = None
+        if cache == E4:
+            self.k_scale, self.v_scale = (torch.rand(Hk, generator=g) * 0.05 + 0.02 for _ in range(2))
+            k, v = k / self.k_scale[:, None], v / self.v_scale[:, None]
+        k, v = k.to(cache), v.to(cache)
+        self.q = (torch.randn((B, Hq, D), generator=g) * q_mul).to(q_dtype)
+        scale = lambda x, s: f64(x) if s is None else f64(x) * s[:, None].double().numpy()  # noqa: E731
+        self.ko, self.vo = scale(k, self.k_scale), scale(v, self.v_scale)
+        self.table, self.lens, self.scale = table, torch.tensor(lens, dtype=torch.int32), 1.0 / (q_mul * D ** 0.5)
+        pool = torch.empty((nb, 2, bs, Hk, D), dtype=cache) if layout == "paired" else None
+        if layout == "paired":
+            pool[:, 0], pool[:, 1] = k, v
+            pool = pool.cuda()
+            self.k, self.v = pool[:, 0], pool[:, 1]
+        elif layout == "heads":
+            self.k, self.v = (x.transpose(1, 2).contiguous().cuda().transpose(1, 2) for x in (k, v))
+        else:
+            self.k, self.v = k.cuda(), v.cuda()
+        self.cache = cache
+
+    def run(self, **kw):
+        dev = lambda x: None if x is None else x.cuda()  # noqa: E731
+        lse = torch.full(self.q.shape[:2], float("nan"), device="cuda")
+        out = kvq.kvq_decode_kv(self.q.cuda(), self.k, self.v, self.table.cuda(), self.lens.cuda(), self.scale,
+                                k_scale=dev(self.k_scale), v_scale=dev(self.v_scale), lse_out=lse,
+                                **{n: dev(x) if isinstance(x, torch.Tensor) and not x.is_cuda else x for n, x in kw.items()})
+        return out, lse
+
+    def oracle(self, sliding_window=0, softcap=0.0, sinks=None, alibi_slopes=None):
+        return paged_kv.decode(f64(self.q), self.ko, self.vo, self.table.numpy(), self.lens.tolist(), self.scale,
+                               sliding_window, softcap, sinks, alibi_slopes)
+
+    def check(self, want=None, flags=0, **kw):
+        out, lse = self.run(**kw)
+        st, got = kvq.kvq_device_error()
+        assert got == flags and st == (kvq.KVQ_ERR_OUT_OF_RANGE if flags else kvq.KVQ_OK)
+        mods = {n: x for n, x in kw.items() if n in ("sliding_window", "softcap", "sinks", "alibi_slopes")}
+        ref, ref_lse, size = want or self.oracle(**mods)
+        err = np.abs(f64(out) - ref)
+        w = 2.0 ** -16 if self.cache == BF else 2.0 ** -11
+        bound = (w + 2.0 ** -12) * size + (torch.finfo(out.dtype).eps / 2 if out.dtype != F32 else 0) * np.abs(ref) * 1.01 + 1e-7
+        assert (err <= bound).all(), "%g times the bound" % np.nanmax(np.where(err <= bound, 0, err / bound))
+        got = f64(lse)
+        fin = np.isfinite(ref_lse)
+        assert np.array_equal(np.isneginf(got), np.isneginf(ref_lse)) and np.isfinite(got[fin]).all()
+        assert (np.abs(got[fin] - ref_lse[fin]) <= 1e-4).all(), np.abs(got[fin] - ref_lse[fin]).max()
+        return out
+
+
+LENS = [0, 1, 15, 16, 17, 100, 33, 700]
+
+
+@pytest.mark.parametrize("cache", [BF, F16, E4])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("Hq,Hk", [(1, 1), (4, 1), (8, 2), (15, 5), (16, 2), (27, 3), (16, 1), (40, 1), (17, 1), (24, 8)])
+def test_heads_and_types(Hq, Hk, D, cache):
+    c = Case(LENS, Hq, Hk, D, cache, seed=Hq + D)
+    want = c.oracle()
+    for S in (0, 1, 5):
+        c.check(want, num_splits=S)
+
+
+@pytest.mark.parametrize("bs", [16, 32, 48, 128])
+@pytest.mark.parametrize("layout", ["apart", "paired", "heads"])
+@pytest.mark.parametrize("cache", [BF, E4])
+def test_blocks_and_layouts(cache, layout, bs):
+    c = Case(LENS + [1029], 8, 2, 128, cache, bs=bs, layout=layout, seed=bs)
+    want = c.oracle()
+    c.check(want)
+    c.check(want, num_splits=7)
+
+
+@pytest.mark.parametrize("q_dtype,out_dtype", list(itertools.product([BF, F16], [BF, F16, F32])))
+def test_query_and_output_types_over_fp8(q_dtype, out_dtype):
+    Case(LENS, 8, 2, 64, E4, q_dtype=q_dtype, seed=3).check(out_dtype=out_dtype)
+    Case(LENS, 8, 2, 64, q_dtype, seed=4).check(out_dtype=out_dtype)
+
+
+@pytest.mark.parametrize("window", [1, 15, 16, 17, 100, 699, 5000])
+@pytest.mark.parametrize("S", [0, 1, 3])
+def test_window(window, S):
+    c = Case(LENS, 12, 3, 64, BF, seed=window)
+    c.check(sliding_window=window, num_splits=S)
+
+
+@pytest.mark.parametrize("cache", [BF, F16, E4])
+@pytest.mark.parametrize("Hq,Hk,D", [(6, 2, 128), (40, 5, 64), (32, 2, 128), (3, 1, 256)])
+def test_modifiers(Hq, Hk, D, cache):
+    g = torch.Generator().manual_seed(9)
+    sinks, slopes = torch.randn(Hq, generator=g) * 2, torch.rand(Hq, generator=g) * 0.1
+    c = Case(LENS, Hq, Hk, D, cache, seed=D)
+    c.check(softcap=2.0)
+    c.check(alibi_slopes=slopes)
+    c.check(sinks=sinks)
+    c.check(sliding_window=37, softcap=5.0, sinks=sinks, alibi_slopes=slopes, num_splits=2)
+    c.check(sliding_window=37, softcap=5.0, sinks=sinks, alibi_slopes=slopes)
+
+
+@pytest.mark.parametrize("lens", [[0], [0, 0, 0], [1], [20000], [3, 9000], [1] * 300, [17] * 513])
+def test_batches(lens):
+    for cache in (BF, E4):
+        c = Case(lens, 8, 4, 64, cache, seed=len(lens))
+        want = c.oracle()
+        for S in (0, 2, 64):
+            c.check(want, num_splits=S)
+
+
+@pytest.mark.parametrize("q_mul", [1e-6, 1e-3, 300.0, 30000.0])
+@pytest.mark.parametrize("q_dtype", [BF, F16])
+def test_query_range_over_fp8(q_mul, q_dtype):
+    if q_dtype == F16 and (q_mul < 1e-3 or q_mul > 10000):
+        q_mul = min(max(q_mul, 1e-2), 10000.0)
+    Case(LENS, 8, 2, 128, E4, q_dtype=q_dtype, seed=5, q_mul=q_mul).check()
+
+
+def test_query_heads_of_different_magnitude_over_fp8():
+    c = Case([40, 500], 8, 2, 64, E4, seed=6)
+    mul = 2.0 ** torch.arange(-20, 12, 4).float()
+    c.q = (c.q.float() * mul[None, :, None]).to(BF)
+    out, lse = c.run()
+    for h in range(8):  # each head as the only one of its size: powers of two change nothing
+        d = Case([40, 500], 8, 2, 64, E4, seed=6)
+        d.q = c.q.clone()
+        d.q[:, [i for i in range(8) if i != h]] = 0
+        o, l = d.run()
+        assert torch.equal(o[:, h], out[:, h]) and torch.equal(l[:, h], lse[:, h])
+
+
+def test_nan_and_infinities_stay_in_their_rows():
+    for cache in (BF, F16, E4):
+        c = Case([40, 33, 20], 8, 2, 64, cache, seed=7)
+        clean, _ = c.run()
+        c.q[1, 2, 5] = float("nan")
+        out, lse = c.run()
+        kvq.kvq_device_error()
+        assert out[1, 2].isnan().all() and lse[1, 2].isnan()
+        keep = torch.ones(3, 8, dtype=torch.bool)
+        keep[1, 2] = False
+        assert torch.equal(out[keep.cuda()], clean[keep.cuda()])
+        # a NaN value of one key reaches its dimension of the heads that read it, and nothing else
+        c = Case([40, 33, 20], 8, 2, 64, cache, seed=7)
+        c.v[c.table[0, 1], 3, 1, 9] = float("nan")
+        out, _ = c.run()
+        hit = torch.zeros(3, 8, 64, dtype=torch.bool)
+        hit[0, 4:, 9] = True
+        assert torch.equal(out.isnan().cpu(), hit) and torch.equal(out[~hit.cuda()], clean[~hit.cuda()])
+
+
+def test_scores_of_minus_infinity():
+    """Keys of the type's lowest value: weights of zero, and a row of nothing else."""
+    c = Case([40, 20], 4, 1, 64, BF, seed=8)
+    c.q = c.q.abs() + 0.1
+    clean = c.oracle()
+    low = torch.finfo(BF).min
+    c.k[c.table[0, 2].item(), 3:8] = low  # scores far below every other key
+    c.ko[c.table[0, 2].item(), 3:8] = -1e30
+    ref = c.oracle()
+    c.check(ref)
+    assert not np.array_equal(ref[0][0], clean[0][0])
+
+
+def test_long_sequence_split():
+    c = Case([50001, 3], 8, 1, 64, F16, seed=10)
+    want = c.oracle()
+    for S in (0, 1, 64):
+        c.check(want, num_splits=S)
+
+
+def test_device_flags():
+    c = Case([40, 100], 4, 2, 64, BF, seed=11)
+    full = c.table.clone()
+    c.table[1, 2] = 10 ** 6
+    out, _ = c.run()
+    assert kvq.kvq_device_error() == (kvq.KVQ_ERR_OUT_OF_RANGE, 1)
+    # the block takes no part: as if its 16 keys were not there
+    d = Case([40, 100], 4, 2, 64, BF, seed=11)
+    d.table[1] = torch.cat((full[1, :2], full[1, 3:], full[1, :1]))
+    d.lens[1] -= 16
+    ref, _, size = d.oracle()
+    assert (np.abs(f64(out) - ref) <= 2.0 ** -11 * size + 2.0 ** -8 * np.abs(ref) * 1.01 + 1e-7).all()
+    c.table = full[:, :3].contiguous()
+    c.check(flags=2)  # 100 keys in 3 blocks: clamped
+    c.lens[0] = -5
+    c.lens[1] = 48
+    c.table[1, 1] = -1
+    out, lse = c.run()
+    assert kvq.kvq_device_error() == (kvq.KVQ_ERR_OUT_OF_RANGE, 1)
+    assert (out[0] == 0).all() and lse[0].isneginf().all()
+
+
+def test_far_blocks():
+    """Byte offsets past 2^32 in both pools."""
+    nb, Hk, D = 160000, 8, 128
+    k, v = (torch.empty((nb, 16, Hk, D), dtype=BF, device="cuda") for _ in range(2))  # 5.2 GB each
+    c = Case([100, 47], 8, 8, D, BF, seed=12)
+    where = torch.randperm(nb - 2, generator=torch.Generator().manual_seed(1))[:c.k.shape[0]] + 1
+    where[0], where[1] = nb - 1, 0
+    k[where.cuda()], v[where.cuda()] = c.k, c.v
+    c.k, c.v = k, v
+    want = c.oracle()
+    c.table = torch.where(c.table >= 0, where[c.table.clamp(min=0).long()].int(), c.table)
+    c.check(want)
+
+
+def test_repeatable_and_on_another_stream_and_captured():
+    c = Case([700, 33, 2000, 0], 16, 4, 128, E4, seed=13)
+    q, table, lens = c.q.cuda(), c.table.cuda(), c.lens.cuda()
+    ks, vs = c.k_scale.cuda(), c.v_scale.cuda()
+    ws = torch.empty(kvq.kvq_decode_kv_workspace_bytes(4, 16, 4, 128), dtype=torch.uint8, device="cuda")
+    outs = [torch.empty_like(q) for _ in range(4)]
+    call = lambda o, **kw: kvq.kvq_decode_kv(q, c.k, c.v, table, lens, c.scale, k_scale=ks, v_scale=vs, out=o, **kw)  # noqa: E731
+    call(outs[0])
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    call(outs[1], stream=side)
+    side.synchronize()
+    step = kvq.CapturedStep(lambda: call(outs[2], workspace=ws), side)
+    step()
+    step2 = kvq.CapturedStep(lambda: call(outs[3], workspace=ws), side)  # a second graph on the same workspace
+    step()
+    step2()
+    side.synchronize()
+    assert all(torch.equal(outs[0], o) for o in outs[1:])
+    lens.clamp_(max=1)  # replays read the lengths of their time (the empty sequence has no block)
+    torch.cuda.synchronize()
+    step()
+    side.synchronize()
+    assert not torch.equal(outs[0], outs[2])
+    c.lens.clamp_(max=1)
+    c.check()
+
+
+def test_binding_checks():
+    c = Case([40, 20], 4, 2, 64, BF, seed=14)
+    q, table, lens = c.q.cuda(), c.table.cuda(), c.lens.cuda()
+    call = lambda **kw: kvq.kvq_decode_kv(**{**dict(q=q, k_cache=c.k, v_cache=c.v, block_table=table, seq_lens=lens,  # noqa: E731
+                                                    softmax_scale=0.1), **kw})
+    ones = torch.ones(2, device="cuda")
+    for kw, err in ((dict(q=q.float()), TypeError), (dict(q=q.half()), TypeError), (dict(q=q[:, :, :32]), ValueError),
+                    (dict(q=q[0]), ValueError), (dict(k_cache=c.k[:, :, :1]), ValueError),
+                    (dict(k_cache=c.k.float(), v_cache=c.v.float()), TypeError), (dict(k_scale=ones), TypeError),
+                    (dict(block_table=table[:1]), ValueError), (dict(seq_lens=lens[:1]), ValueError),
+                    (dict(seq_lens=lens.long()), TypeError), (dict(out=q[:1]), ValueError), (dict(sinks=ones), ValueError),
+                    (dict(lse_out=torch.empty(2, 3, device="cuda")), ValueError), (dict(softmax_scale=0.0), kvq.KvqError),
+                    (dict(workspace=torch.empty(64, dtype=torch.uint8, device="cuda")), kvq.KvqError)):
+        with pytest.raises(err):
+            call(**kw)

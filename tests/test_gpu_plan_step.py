@@ -1,0 +1,173 @@
+"""kvq_plan_step against the request-by-request oracle (whole numbers: equal)."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import paged_kv
+from quantized_paged_kv_int4_gb300 import kvq
+
+pytestmark = pytest.mark.gpu
+
+
+def _i32(x):
+    return torch.as_tensor(np.asarray(x), dtype=torch.int32).cuda()
+
+
+def _inputs(context, query, bs, width, seed, spare=3, first=2, shuffle=True):
+    """(table, free, cursor, rows, num_blocks): the requests' blocks, the rest of the pool as the free list."""
+    rng = np.random.default_rng(seed)
+    B = len(context)
+    have = [min(-(-max(int(c), 0) // bs), width) for c in context]  # what a row can hold
+    need = [-(-(max(int(c), 0) + max(int(n), 0)) // bs) for c, n in zip(context, query)]
+    ids = rng.permutation(sum(need) + spare + first)
+    rows = rng.permutation(B + 4)[:B] if shuffle else np.arange(B)
+    table = np.full((B + 4, width), -1)
+    at = 0
+    for b in range(B):
+        table[rows[b], :have[b]] = ids[at:at + have[b]]
+        at += have[b]
+    return table, ids[at:], first, rows, len(ids)
+
+
+def _check(context, query, bs=16, width=None, pad=0, T=None, seed=0, in_place=False, shuffle=True, batch=True, free=True,
+           single=False):
+    context, query = list(context), list(query)
+    width = width or max([-(-(c + n) // bs) for c, n in zip(context, query)] + [1]) + 2
+    table, ids, cursor, rows, nb = _inputs(context, query, bs, width, seed, shuffle=shuffle)
+    if not free:  # the table holds every block already
+        for b, r in enumerate(rows):
+            table[r, :] = np.random.default_rng(seed + b).permutation(max(nb, width))[:width] % nb
+    T = sum(query) + pad if T is None else T
+    g_table, g_batch = _i32(table), torch.full((len(context), width), -7, dtype=torch.int32, device="cuda")
+    g_cursor = torch.tensor([cursor], device="cuda")
+    g_out = g_cursor if in_place else torch.full((1,), -1, device="cuda")
+    o_table, o_batch = table.copy(), np.full((len(context), width), -7)
+    want = paged_kv.plan_step(context, None if single else query, o_table, ids if free else None, cursor, bs, nb, T,
+                              rows=rows if shuffle else None, batch=o_batch)
+    got = kvq.kvq_plan_step(_i32(context), None if single else _i32(query), g_table, _i32(ids) if free else None,
+                            g_cursor if free else None, bs, nb, rows=_i32(rows) if shuffle else None,
+                            batch_table=g_batch if batch else None, cursor_out=g_out if free else None, T=T)
+    st, flags = kvq.kvq_device_error()
+    for name, x, y in zip(("seq_lens", "query_start_loc", "positions", "slot_mapping"), got, want):
+        assert np.array_equal(x.cpu().numpy(), y), name
+    assert np.array_equal(g_table.cpu().numpy(), o_table), "block_table"
+    if batch:
+        assert np.array_equal(g_batch.cpu().numpy(), o_batch), "batch_table"
+    if free:
+        assert int(g_out) == want[4], "cursor"
+        assert in_place or int(g_cursor) == cursor
+    assert flags == want[5] and st == (kvq.KVQ_ERR_OUT_OF_RANGE if flags else kvq.KVQ_OK)
+    return flags
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("context,query", [
+    ([0], [1]), ([16], [1]), ([15], [1]), ([31], [2]), ([0], [0]), ([5], [0]),
+    ([0, 16, 15, 33, 1024], [1, 1, 1, 1, 1]),
+    ([0, 7, 0, 100, 16, 0], [40, 0, 16, 1, 17, 0]),
+])
+def test_small_steps(context, query, in_place):
+    assert _check(context, query, pad=3, seed=len(context), in_place=in_place) == 0
+
+
+@pytest.mark.parametrize("bs", [1, 3, 16, 64])
+@pytest.mark.parametrize("B,chunk,in_place", [(1, 5000, True), (37, 300, False), (300, 40, True), (1031, 1, False)])
+def test_random_steps(B, chunk, bs, in_place):
+    rng = np.random.default_rng(B + bs)
+    context = rng.integers(0, 700, B).tolist()
+    query = rng.integers(0, chunk + 1, B).tolist()
+    assert _check(context, query, bs=bs, pad=B % 7, seed=B, in_place=in_place) == 0
+
+
+def test_most_requests():
+    rng = np.random.default_rng(5)
+    assert _check(rng.integers(0, 60, 8192).tolist(), [1] * 8192, seed=1, in_place=True, single=True) == 0
+
+
+def test_rows_in_order_no_batch_table_no_free_list():
+    assert _check([3, 40, 0], [1, 20, 33], shuffle=False) == 0
+    assert _check([3, 40, 0], [1, 20, 33], batch=False) == 0
+    assert _check([3, 40, 0], [1, 20, 33], free=False) == 0
+    assert _check([3, 40, 15], [1, 1, 1], single=True) == 0
+
+
+def test_no_requests():
+    slots = torch.full((5,), 9, dtype=torch.int64, device="cuda")
+    seq, starts, pos, _ = kvq.kvq_plan_step(_i32([]), None, _i32(np.zeros((1, 1))), None, None, 16, 4, slot_mapping=slots)
+    assert starts.tolist() == [0] and pos.tolist() == [-1] * 5 and slots.tolist() == [-1] * 5 and seq.numel() == 0
+    assert kvq.kvq_device_error() == (0, 0)
+
+
+def test_faults_are_flagged_and_nothing_leaves_the_buffers():
+    assert _check([20, -5, 3], [2, 4, -1]) == 2                      # negative lengths
+    assert _check([20, 30], [2, 30], width=3) == 2                  # a sequence past its row
+    assert _check([20, 200], [2, 30], width=3) == 2                 # held tokens past the row too
+    assert _check([20, 30], [20, 30], T=33) == 2                    # more tokens than rows
+    # the free list runs out, and a bad id in it
+    context, query = _i32([0, 10]), _i32([40, 40])
+    for ids, flag, cur in (([3, 4, 5], 32, 3), ([3, 99, 5, 1, 0, 2, 6], 1, 6), ([3, -1, 5, 1, 0, 2, 6], 1, 6)):
+        o_table = np.full((2, 8), -1)
+        o_table[1, 0] = 7
+        g_table, cursor = _i32(o_table), torch.zeros(1, dtype=torch.int64, device="cuda")
+        want = paged_kv.plan_step([0, 10], [40, 40], o_table, ids, 0, 16, 8, 90)
+        got = kvq.kvq_plan_step(context, query, g_table, _i32(ids), cursor, 16, 8, T=90)
+        for x, y in zip(got, want):
+            assert np.array_equal(x.cpu().numpy(), y)
+        assert np.array_equal(g_table.cpu().numpy(), o_table) and int(cursor) == want[4] == cur
+        assert kvq.kvq_device_error() == (kvq.KVQ_ERR_OUT_OF_RANGE, flag) and want[5] == flag
+    # a bad row, and a bad id in a held block
+    o_table = np.array([[1, 2, -1, -1], [9, 3, -1, -1]])
+    g_table, cursor = _i32(o_table), torch.zeros(1, dtype=torch.int64, device="cuda")
+    want = paged_kv.plan_step([20, 5, 20], [2, 3, 2], o_table, [4, 5], 0, 16, 8, 9, rows=[0, 2, 1])
+    got = kvq.kvq_plan_step(_i32([20, 5, 20]), _i32([2, 3, 2]), g_table, _i32([4, 5]), cursor, 16, 8, rows=_i32([0, 2, 1]),
+                            T=9)
+    for x, y in zip(got, want):
+        assert np.array_equal(x.cpu().numpy(), y)
+    assert kvq.kvq_device_error() == (kvq.KVQ_ERR_OUT_OF_RANGE, 1) and want[5] == 1
+
+
+def test_captured_step_advances_its_cursor():
+    """One graph, replayed: lengths and cursor advance on the device."""
+    B, bs, steps = 3, 16, 40
+    context, table = _i32([0, 15, 30]), _i32([[-1] * 6, [50] + [-1] * 5, [51, 52] + [-1] * 4])
+    free, cursor = _i32(np.arange(40)), torch.zeros(1, dtype=torch.int64, device="cuda")
+    pos, slots = torch.empty(B, dtype=torch.int32, device="cuda"), torch.empty(B, dtype=torch.int64, device="cuda")
+    seq = torch.empty(B, dtype=torch.int32, device="cuda")
+    stream = torch.cuda.Stream()
+
+    def step():
+        kvq.kvq_plan_step(context, None, table, free, cursor, bs, 60, seq_lens=seq, positions=pos, slot_mapping=slots)
+        context.copy_(seq)
+
+    stream.wait_stream(torch.cuda.current_stream())
+    run = kvq.CapturedStep(step, stream)  # runs once eagerly
+    o_table, o_context, o_cursor = np.array([[-1] * 6, [50] + [-1] * 5, [51, 52] + [-1] * 4]), [0, 15, 30], 0
+    for i in range(steps):
+        if i:
+            run()
+        want = paged_kv.plan_step(o_context, None, o_table, list(range(40)), o_cursor, bs, 60, B)
+        o_context, o_cursor = want[0].tolist(), want[4]
+        stream.synchronize()
+        assert np.array_equal(slots.cpu().numpy(), want[3]) and np.array_equal(pos.cpu().numpy(), want[2]), i
+    assert int(cursor) == o_cursor and np.array_equal(table.cpu().numpy(), o_table)
+    assert kvq.kvq_device_error() == (0, 0)
+
+
+def test_binding_checks():
+    c, t = _i32([1, 2]), _i32(np.zeros((2, 4)))
+    cur = torch.zeros(1, dtype=torch.int64, device="cuda")
+    with pytest.raises(ValueError):
+        kvq.kvq_plan_step(c, None, t, None, None, 16, 4)                        # no T
+    with pytest.raises(ValueError):
+        kvq.kvq_plan_step(c, None, t, _i32([1]), None, 16, 4, T=2)              # free list without a cursor
+    with pytest.raises(ValueError):
+        kvq.kvq_plan_step(c, _i32([1]), t, None, None, 16, 4, T=2)              # query_lens of another size
+    with pytest.raises(ValueError):
+        kvq.kvq_plan_step(c, None, t, _i32([1]), cur, 16, 4, T=2, batch_table=_i32(np.zeros((2, 3))))
+    with pytest.raises(TypeError):
+        kvq.kvq_plan_step(c, None, t, _i32([1]), cur.int(), 16, 4, T=2)
+    with pytest.raises(kvq.KvqError):
+        kvq.kvq_plan_step(c, None, t, _i32([1]), cur, 16, 4, T=2, batch_table=t)  # the table itself
+    with pytest.raises(kvq.KvqError):
+        kvq.kvq_plan_step(c, None, t, _i32([1]), cur, 16, 4, T=2, seq_lens=c)

@@ -1,0 +1,226 @@
+"""kvq_rope and kvq_write_kv against the float64 oracle.
+
+Bounds, for an element whose pair is (a, b) and whose result is y:
+  rotation: cos and sin from an angle known to 2^-25 turns of rounding (2 pi 2^-25 < 2^-22) by a function good
+    to 2 units in the last place (2^-22), two products and a sum (3 * 2^-24): below 2^-20 (|a| + |b|) factor;
+  output: half a step of the type, eps / 2 |y| (below the smallest normal: half of the smallest step).
+An FP8 code is the one of some value that close to y / scale (one more fp32 rounding, the division): it lies
+between the codes of the two ends. Rows that only pass (values, elements past the rotated ones, 16-bit) are equal."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import paged_kv
+from quantized_paged_kv_int4_gb300 import kvq
+
+pytestmark = pytest.mark.gpu
+
+BF, F16, F32, E4 = torch.bfloat16, torch.float16, torch.float32, torch.float8_e4m3fn
+TINY = {BF: 2.0 ** -134, F16: 2.0 ** -25, F32: 2.0 ** -150}
+
+
+def f64(x):
+    return x.detach().float().cpu().double().numpy()
+
+
+def close(got, want, size, dtype, what):
+    err = np.abs(f64(got) - want)
+    bound = 2.0 ** -20 * size + torch.finfo(dtype).eps / 2 * np.abs(want) * (1 + 2.0 ** -18) + TINY[dtype]
+    assert (err <= bound).all(), "%s: %g times the bound" % (what, (err / bound).max())
+
+
+def freqs_of(R, base=10000.0, **kw):
+    return kvq.kvq_rope_frequencies(R, base, device="cuda", **kw)
+
+
+def positions_of(T, seed, pad=0, high=40000):
+    g = torch.Generator().manual_seed(seed)
+    pos = torch.randint(0, high, (T,), generator=g, dtype=torch.int32)
+    pos[:1] = 0
+    if T > 3:
+        pos[1], pos[2] = 1000003, 2 ** 31 - 1
+    if pad:
+        pos[T - pad:] = torch.tensor([-1, -5, -(2 ** 31)])[torch.arange(pad) % 3].int()
+    return pos
+
+
+@pytest.mark.parametrize("dtype", [BF, F16, F32])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("D,R", [(128, 128), (128, 64), (64, 64), (80, 80), (80, 40), (256, 32), (64, 2), (24, 20), (7, 6),
+                                 (1024, 1024)])
+def test_rope(D, R, interleaved, dtype):
+    T, Hq, Hk, pad = 13, 5, 2, 3
+    x = torch.randn((T, (Hq + Hk) * D), generator=torch.Generator().manual_seed(D + R)).to(dtype).cuda()
+    q, k = (y.unflatten(1, (-1, D)) for y in x.split([Hq * D, Hk * D], 1))  # views of a fused projection
+    pos = positions_of(T, R, pad)
+    freqs, _ = freqs_of(R)
+    mark = [torch.full((T, h, D), 77.0, dtype=dtype, device="cuda") for h in (Hq, Hk)]
+    out = kvq.kvq_rope(q, k, pos.cuda(), freqs, interleaved=interleaved, attn_factor=1.25, q_out=mark[0], k_out=mark[1])
+    assert out[0] is mark[0] and out[1] is mark[1]
+    live = T - pad
+    for got, inp, n in zip(out, (q, k), "qk"):
+        want, size = paged_kv.rotate(f64(inp[:live]), pos[:live].tolist(), freqs.tolist(), interleaved, 1.25)
+        close(got[:live], want, size, dtype, n)
+        assert torch.equal(got[:live, :, R:], inp[:live, :, R:])
+        assert (got[live:] == 77.0).all()  # padding stays as it was
+    # in place gives the same bits
+    y = x.clone()
+    q2, k2 = (z.unflatten(1, (-1, D)) for z in y.split([Hq * D, Hk * D], 1))
+    kvq.kvq_rope(q2, k2, pos.cuda(), freqs, interleaved=interleaved, attn_factor=1.25, q_out=q2, k_out=k2)
+    assert torch.equal(q2[:live], out[0][:live]) and torch.equal(k2[:live], out[1][:live])
+    assert torch.equal(y[live:], x[live:])
+    # one of the two alone
+    only, none = kvq.kvq_rope(q, None, pos.cuda(), freqs, interleaved=interleaved, attn_factor=1.25)
+    assert none is None and torch.equal(only[:live], out[0][:live])
+    none, only = kvq.kvq_rope(None, k, pos.cuda(), freqs, interleaved=interleaved, attn_factor=1.25)
+    assert none is None and torch.equal(only[:live], out[1][:live])
+
+
+@pytest.mark.parametrize("shift", [1, 2, 4])
+def test_rope_odd_strides_and_offsets(shift):
+    """Rows that start off 16-byte boundaries, padded heads and tokens in another order."""
+    T, H, D, R = 9, 3, 64, 64
+    pool = torch.randn((H, T, D + 5), generator=torch.Generator().manual_seed(shift)).to(BF).cuda()
+    q = pool.flatten()[shift:shift + H * T * (D + 5) - 8].as_strided((T, H, D), (D + 5, T * (D + 5), 1), shift)[:-1]
+    pos, (freqs, _) = positions_of(T - 1, 3).cuda(), freqs_of(R)
+    got, _ = kvq.kvq_rope(q, None, pos, freqs)
+    want, size = paged_kv.rotate(f64(q), pos.tolist(), freqs.tolist(), False, 1.0)
+    close(got, want, size, BF, "q")
+
+
+@pytest.mark.parametrize("scaling", ["linear", "bands", "yarn"])
+def test_rope_long_context_scaling(scaling):
+    freqs, factor = freqs_of(64, 500000.0, scaling=scaling, factor=16.0, original=4096)
+    q = torch.randn((5, 2, 64), generator=torch.Generator().manual_seed(1)).cuda()
+    pos = torch.tensor([0, 1, 4097, 65535, 1 << 20], dtype=torch.int32)
+    got, _ = kvq.kvq_rope(q, None, pos.cuda(), freqs, attn_factor=factor)
+    want, size = paged_kv.rotate(f64(q), pos.tolist(), freqs.tolist(), False, factor)
+    close(got, want, size, F32, scaling)
+
+
+def test_rope_single_token_and_none():
+    q, (freqs, _) = torch.randn((1, 1, 128)).to(BF).cuda(), freqs_of(128)
+    got, _ = kvq.kvq_rope(q, None, torch.tensor([7], dtype=torch.int32).cuda(), freqs)
+    want, size = paged_kv.rotate(f64(q), [7], freqs.tolist(), False, 1.0)
+    close(got, want, size, BF, "one")
+    empty, _ = kvq.kvq_rope(q[:0], None, torch.zeros(0, dtype=torch.int32).cuda(), freqs)
+    assert empty.shape == (0, 1, 128)
+
+
+def pool_of(nb, bs, Hk, D, layout, dtype, fill=3.0):
+    if layout == "paired":
+        kv = torch.full((nb, 2, bs, Hk, D), fill, dtype=torch.float32, device="cuda").to(dtype)
+        return kv[:, 0], kv[:, 1]
+    if layout == "heads":
+        return tuple(torch.full((nb, Hk, bs, D), fill, dtype=torch.float32, device="cuda").to(dtype).transpose(1, 2) for _ in "kv")
+    return tuple(torch.full((nb, bs, Hk, D), fill, dtype=torch.float32, device="cuda").to(dtype) for _ in "kv")
+
+
+def codes_close(got, x, size, scale, what):
+    """got: FP8 values; x: exact values before the division by scale [Hk, 1]."""
+    off = (2.0 ** -20 * size + 2.0 ** -23 * np.abs(x)) / scale
+    lo, hi = paged_kv.e4m3(x / scale - off), paged_kv.e4m3(x / scale + off)
+    g = f64(got)
+    assert ((g >= lo) & (g <= hi)).all(), what
+
+
+@pytest.mark.parametrize("layout", ["apart", "paired", "heads"])
+@pytest.mark.parametrize("dtype,cache", [(BF, BF), (F16, F16), (BF, E4), (F16, E4)])
+@pytest.mark.parametrize("T,Hq,Hk,D,R,bs,interleaved", [
+    (1, 4, 1, 128, 128, 16, False), (37, 8, 2, 64, 64, 16, True), (50, 6, 3, 128, 64, 32, False),
+    (21, 5, 5, 256, 256, 48, True), (19, 4, 2, 80, 40, 7, False), (70, 32, 8, 128, 128, 16, False), (8, 2, 1, 16, 12, 1, True),
+])
+def test_write_kv(T, Hq, Hk, D, R, bs, interleaved, dtype, cache, layout):
+    g = torch.Generator().manual_seed(T + D)
+    x = (torch.randn((T, (Hq + 2 * Hk) * D), generator=g) * 2).to(dtype).cuda()
+    q, k, v = (y.unflatten(1, (-1, D)) for y in x.split([Hq * D, Hk * D, Hk * D], 1))
+    pad = 2 if T > 8 else 0
+    pos, (freqs, _) = positions_of(T, T, pad), freqs_of(R)
+    nb = -(-T // bs) + 2
+    slots = torch.randperm(nb * bs, generator=g)[:T]
+    slots[3:5] = -1  # live tokens that are not cached: only their query is rotated
+    kc, vc = pool_of(nb, bs, Hk, D, layout, cache)
+    ks = vs = None
+    if cache == E4:
+        ks, vs = torch.rand(Hk, generator=g) * 0.05 + 0.005, torch.rand(Hk, generator=g) * 0.05 + 0.005
+    q_out = torch.full((T, Hq, D), 77.0, dtype=dtype, device="cuda")
+    kvq.kvq_write_kv(k, v, kc, vc, slots.cuda(), k_scale=None if ks is None else ks.cuda(),
+                     v_scale=None if vs is None else vs.cuda(), q=q, positions=pos.cuda(), freqs=freqs,
+                     interleaved=interleaved, attn_factor=0.75, q_out=q_out)
+    assert kvq.kvq_device_error() == (0, 0)
+    live = T - pad
+    want, size = paged_kv.rotate(f64(q[:live]), pos[:live].tolist(), freqs.tolist(), interleaved, 0.75)
+    close(q_out[:live], want, size, dtype, "q")
+    assert (q_out[live:] == 77.0).all()
+    put = [t for t in range(live) if slots[t] >= 0]
+    at = slots[put]
+    kg, vg = (c.float()[(at // bs).cuda(), (at % bs).cuda()] for c in (kc, vc))
+    want, size = paged_kv.rotate(f64(k[put]), pos[put].tolist(), freqs.tolist(), interleaved, 0.75)
+    if cache == E4:
+        codes_close(kg, want, size, ks[:, None].double().numpy(), "k")
+        codes_close(vg, f64(v[put]), 0 * f64(v[put]), vs[:, None].double().numpy(), "v")
+    else:
+        close(kg, want, size, dtype, "k")
+        assert torch.equal(vg, v[put].float())
+    untouched = torch.ones((nb, bs), dtype=torch.bool)
+    untouched[at // bs, at % bs] = False
+    start = torch.tensor(3.0).to(cache).float().item()
+    assert all((c.float()[untouched.cuda()] == start).all() for c in (kc, vc))
+
+
+def test_write_without_rotation_is_a_copy():
+    T, Hk, D, bs = 33, 4, 128, 16
+    k, v = (torch.randn((T, Hk, D), generator=torch.Generator().manual_seed(i)).to(BF).cuda() for i in (1, 2))
+    kc, vc = pool_of(4, bs, Hk, D, "apart", BF)
+    slots = torch.arange(T).flip(0).cuda()
+    slots[5] = 4 * bs + 2  # past the pool
+    assert kvq.kvq_write_kv(k, v, kc, vc, slots) is None
+    assert kvq.kvq_device_error() == (kvq.KVQ_ERR_OUT_OF_RANGE, 4)
+    keep = [t for t in range(T) if t != 5]
+    for c, x in ((kc, k), (vc, v)):
+        assert torch.equal(c.flatten(0, 1)[slots[keep]], x[keep])
+
+
+def test_fp8_write_saturates_and_keeps_nan():
+    x = torch.tensor([1e30, -1e30, float("inf"), float("-inf"), float("nan"), 447.9, 464.0, 2.0 ** -10]).repeat(2)[None, None]
+    kc, vc = pool_of(1, 16, 1, 16, "apart", E4)
+    kvq.kvq_write_kv(x.to(BF).cuda(), x.to(BF).cuda(), kc, vc, torch.zeros(1, dtype=torch.int64).cuda())
+    want = paged_kv.e4m3(f64(x.to(BF))[0, 0])
+    assert np.array_equal(f64(kc)[0, 0, 0], want, equal_nan=True) and np.array_equal(f64(vc)[0, 0, 0], want, equal_nan=True)
+
+
+def test_write_far_blocks():
+    """Offsets past 2^32 bytes."""
+    nb, bs, Hk, D = 70000, 16, 8, 256
+    kc = torch.empty((nb, bs, Hk, D), dtype=BF, device="cuda")  # 4.6 GB
+    vc = torch.empty((nb, bs, Hk, D), dtype=BF, device="cuda")
+    k, v = (torch.randn((3, Hk, D), generator=torch.Generator().manual_seed(i)).to(BF).cuda() for i in (1, 2))
+    slots = torch.tensor([nb * bs - 1, 0, (nb - 3) * bs + 5]).cuda()
+    kvq.kvq_write_kv(k, v, kc, vc, slots)
+    for c, x in ((kc, k), (vc, v)):
+        assert torch.equal(c[slots // bs, slots % bs], x)
+    assert kvq.kvq_device_error() == (0, 0)
+
+
+def test_binding_checks():
+    x = torch.zeros((4, 2, 64), dtype=BF, device="cuda")
+    pos, (freqs, _) = torch.zeros(4, dtype=torch.int32, device="cuda"), freqs_of(64)
+    kc, vc = pool_of(1, 16, 2, 64, "apart", BF)
+    slots = torch.zeros(4, dtype=torch.int64, device="cuda")
+    for call, err in ((lambda: kvq.kvq_rope(x, x.half(), pos, freqs), TypeError),
+                      (lambda: kvq.kvq_rope(x, x[:3], pos, freqs), ValueError),
+                      (lambda: kvq.kvq_rope(x, None, pos[:3], freqs), ValueError),
+                      (lambda: kvq.kvq_rope(x, None, pos, freqs_of(128)[0]), ValueError),
+                      (lambda: kvq.kvq_rope(x, None, pos, freqs, q_out=x[:, :1]), ValueError),
+                      (lambda: kvq.kvq_rope(x, None, pos, freqs, k_out=x), ValueError),
+                      (lambda: kvq.kvq_rope(x, None, pos, freqs.cpu()), TypeError),
+                      (lambda: kvq.kvq_write_kv(x, x, kc.half(), vc.half(), slots), TypeError),
+                      (lambda: kvq.kvq_write_kv(x, x, kc, vc[:, :8], slots), ValueError),
+                      (lambda: kvq.kvq_write_kv(x[:, :1], x[:, :1], kc, vc, slots), ValueError),
+                      (lambda: kvq.kvq_write_kv(x, x, kc, vc, slots[:2]), ValueError),
+                      (lambda: kvq.kvq_write_kv(x, x, kc, vc, slots, k_scale=torch.ones(2, device="cuda")), TypeError),
+                      (lambda: kvq.kvq_write_kv(x, x, kc, vc, slots, q=x), ValueError),
+                      (lambda: kvq.kvq_write_kv(x, x, kc, vc, slots, positions=pos), ValueError)):
+        with pytest.raises(err):
+            call()

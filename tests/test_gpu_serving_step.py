@@ -1,0 +1,144 @@
+"""The operators together, as a serving loop uses them: plan, rotate and write, decode."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import int4_cache, paged_kv
+from quantized_paged_kv_int4_gb300 import kvq, workloads
+
+pytestmark = pytest.mark.gpu
+
+BF, E4 = torch.bfloat16, torch.float8_e4m3fn
+
+
+def f64(x):
+    return x.detach().float().cpu().double().numpy()
+
+
+@pytest.mark.parametrize("cache,bs,Hq,Hk,D", [(BF, 16, 8, 2, 64), (E4, 32, 12, 3, 128), (torch.float16, 16, 4, 4, 128)])
+def test_prefill_then_decode(cache, bs, Hq, Hk, D):
+    """Requests arrive with prompts of different lengths, then take one token a step. At every decode step
+    the output is the attention over all tokens so far of keys rotated to their positions. The bound is that of
+    the decode (test_gpu_decode_kv.py) on the values that the cache holds; those are checked against the rotation."""
+    dtype = BF if cache == E4 else cache
+    prompts, steps, width = [5, 40, 1, 17], 20, 6
+    B, nb = len(prompts), 40
+    g = torch.Generator().manual_seed(1)
+    dev = dict(device="cuda")
+    freqs, _ = kvq.kvq_rope_frequencies(D, 10000.0, device="cuda")
+    kc, vc = (torch.zeros((nb, bs, Hk, D), **dev).to(cache) for _ in range(2))
+    ks = vs = None
+    if cache == E4:
+        ks, vs = torch.full((Hk,), 0.02, **dev), torch.full((Hk,), 0.03, **dev)
+    table = torch.full((B, width), -1, dtype=torch.int32, **dev)
+    free = torch.randperm(nb, generator=g).to(torch.int32).cuda()
+    cursor = torch.zeros(1, dtype=torch.int64, **dev)
+    context = torch.zeros(B, dtype=torch.int32, **dev)
+    new = torch.tensor(prompts, dtype=torch.int32, **dev)
+    keys, values = [[] for _ in range(B)], [[] for _ in range(B)]
+    for step in range(steps):
+        count = prompts if step == 0 else [1] * B
+        T = sum(count) + 3  # a padded batch
+        x = torch.randn((T, (Hq + 2 * Hk), D), generator=g).to(dtype).cuda()
+        q, k, v = x.split([Hq, Hk, Hk], 1)
+        lens, starts, pos, slots = kvq.kvq_plan_step(context, new, table, free, cursor, bs, nb, T=T)
+        q_out = kvq.kvq_write_kv(k, v, kc, vc, slots, k_scale=ks, v_scale=vs, q=q, positions=pos, freqs=freqs)
+        at = 0
+        for b, n in enumerate(count):
+            p = list(range(int(context[b]), int(context[b]) + n))
+            rot, _ = paged_kv.rotate(f64(k[at:at + n]), p, freqs.tolist(), False, 1.0)
+            keys[b].append(rot)
+            values[b].append(f64(v[at:at + n]))
+            at += n
+        last = starts[1:].long() - 1
+        out = kvq.kvq_decode_kv(q_out[last], kc, vc, table, lens, D ** -0.5, k_scale=ks, v_scale=vs)
+        context.copy_(lens)
+        new.fill_(1)
+        assert kvq.kvq_device_error() == (0, 0)
+        # the cache holds the rotated keys and the values, half a step of its type off
+        scale = lambda c, s: f64(c) if s is None else f64(c) * s[:, None].double().cpu().numpy()  # noqa: E731
+        ko, vo = scale(kc, ks), scale(vc, vs)
+        t = table.cpu().numpy()
+        for b in range(B):
+            n = np.arange(int(lens[b]))
+            for held, made, s in ((ko, keys[b], ks), (vo, values[b], vs)):
+                made = np.concatenate(made)
+                got = held[t[b, n // bs], n % bs]
+                low = 0 if s is None else float(s[0]) * 2.0 ** -10
+                assert (np.abs(got - made) <= torch.finfo(cache).eps / 2 * np.abs(made) * 1.001 + 1e-5 + low).all()
+        ref, _, size = paged_kv.decode(f64(q_out[last]), ko, vo, t, lens.tolist(), D ** -0.5)
+        w = 2.0 ** -16 if cache == BF else 2.0 ** -11
+        bound = (w + 2.0 ** -12) * size + torch.finfo(dtype).eps / 2 * np.abs(ref) * 1.01 + 1e-7
+        assert (np.abs(f64(out) - ref) <= bound).all(), step
+
+
+def test_rotary_and_plan_before_the_int4_cache():
+    """The same plan and rotation in front of the INT4 write and decode: the cache bytes equal the oracle's write
+    of the rotated keys, and the decode agrees with the oracle on them."""
+    Hq, Hk, D, bs, nb, prompts = 8, 2, 128, 16, 20, [33, 7, 100]
+    g = torch.Generator().manual_seed(2)
+    B, T = len(prompts), sum(prompts)
+    x = torch.randn((T, Hq + 2 * Hk, D), generator=g).to(BF).cuda()
+    q, k, v = x.split([Hq, Hk, Hk], 1)
+    signs = workloads.rht_signs(D)
+    freqs, _ = kvq.kvq_rope_frequencies(D, 500000.0, device="cuda")
+    table = torch.full((B, 8), -1, dtype=torch.int32, device="cuda")
+    free, cursor = torch.randperm(nb, generator=g).to(torch.int32).cuda(), torch.zeros(1, dtype=torch.int64, device="cuda")
+    context, new = torch.zeros(B, dtype=torch.int32).cuda(), torch.tensor(prompts, dtype=torch.int32).cuda()
+    lens, starts, pos, slots = kvq.kvq_plan_step(context, new, table, free, cursor, bs, nb, T=T)
+    q_rot, k_rot = kvq.kvq_rope(q, k, pos, freqs)
+    kc, vc = (torch.zeros((nb, bs, Hk, D // 2), dtype=torch.uint8, device="cuda") for _ in range(2))
+    ks, vs = (torch.zeros((nb, bs, Hk), device="cuda") for _ in range(2))
+    kvq.kvq_write_int4(k_rot, v, kc, vc, ks, vs, slots, signs.cuda())
+    last = starts[1:].long() - 1
+    out = kvq.kvq_decode_int4(q_rot[last], kc, vc, ks, vs, table, lens, signs.cuda(), D ** -0.5)
+    assert kvq.kvq_device_error() == (0, 0)
+    okc, ovc = (np.zeros(tuple(kc.shape), np.uint8) for _ in range(2))
+    oks, ovs = (np.zeros((nb, bs, Hk), np.uint32) for _ in range(2))
+    f32 = workloads.to_numpy_f32
+    int4_cache.write_int4(f32(k_rot), f32(v), slots.cpu().numpy(), signs.numpy(), okc, ovc, oks, ovs)
+    assert np.array_equal(kc.cpu().numpy(), okc) and np.array_equal(vc.cpu().numpy(), ovc)
+    ref = int4_cache.decode_int4(f32(q_rot[last]), okc, ovc, oks, ovs, table.cpu().numpy(), np.array(prompts), signs.numpy(),
+                                 D ** -0.5)
+    assert (np.abs(f64(out) - ref) <= 2e-3 + 1e-2 * np.abs(ref)).all()
+
+
+def test_captured_serving_step():
+    """Plan, write and decode in one graph, replayed over many steps, against the same steps run eagerly."""
+    Hq, Hk, D, bs, nb, B, steps = 8, 2, 128, 16, 40, 3, 40
+    dev = dict(device="cuda")
+    freqs, _ = kvq.kvq_rope_frequencies(D, 10000.0, device="cuda")
+    xs = torch.randn((steps, B, Hq + 2 * Hk, D), generator=torch.Generator().manual_seed(3)).to(BF).cuda()
+
+    def fresh():
+        return dict(kc=torch.zeros((nb, bs, Hk, D), dtype=BF, **dev), vc=torch.zeros((nb, bs, Hk, D), dtype=BF, **dev),
+                    table=torch.full((B, 8), -1, dtype=torch.int32, **dev), cursor=torch.zeros(1, dtype=torch.int64, **dev),
+                    free=torch.arange(nb, dtype=torch.int32, **dev), context=torch.zeros(B, dtype=torch.int32, **dev),
+                    x=xs[0].clone(), out=torch.empty((B, Hq, D), dtype=BF, **dev), lens=torch.empty(B, dtype=torch.int32, **dev),
+                    pos=torch.empty(B, dtype=torch.int32, **dev), slots=torch.empty(B, dtype=torch.int64, **dev),
+                    q=torch.empty((B, Hq, D), dtype=BF, **dev),
+                    ws=torch.empty(kvq.kvq_decode_kv_workspace_bytes(B, Hq, Hk, D), dtype=torch.uint8, **dev))
+
+    def step(s):
+        q, k, v = s["x"].split([Hq, Hk, Hk], 1)
+        kvq.kvq_plan_step(s["context"], None, s["table"], s["free"], s["cursor"], bs, nb, seq_lens=s["lens"],
+                          positions=s["pos"], slot_mapping=s["slots"])
+        kvq.kvq_write_kv(k, v, s["kc"], s["vc"], s["slots"], q=q, positions=s["pos"], freqs=freqs, q_out=s["q"])
+        kvq.kvq_decode_kv(s["q"], s["kc"], s["vc"], s["table"], s["lens"], D ** -0.5, out=s["out"], workspace=s["ws"])
+        s["context"].copy_(s["lens"])
+
+    a, b = fresh(), fresh()
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    run = kvq.CapturedStep(lambda: step(b), stream)  # runs once
+    for i in range(steps):
+        a["x"].copy_(xs[i])
+        step(a)
+        if i:
+            with torch.cuda.stream(stream):
+                b["x"].copy_(xs[i])
+            run()
+        torch.cuda.synchronize()
+        assert torch.equal(a["out"], b["out"]) and torch.equal(a["table"], b["table"]), i
+    assert int(a["context"][0]) == steps and torch.equal(a["kc"], b["kc"]) and kvq.kvq_device_error() == (0, 0)

@@ -1,0 +1,254 @@
+"""The serving-step operators without a GPU: rotary frequencies (a host function), the oracle against
+independent forms, and the refusals of the C entries. Every call below is refused before a launch (or has
+nothing to do), so the fake pointers are never used."""
+
+import ctypes
+import math
+from fractions import Fraction
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import paged_kv
+from quantized_paged_kv_int4_gb300 import kvq
+
+BAD, UNSUP, OK = kvq.KVQ_ERR_INVALID_ARG, kvq.KVQ_ERR_UNSUPPORTED, kvq.KVQ_OK
+
+
+# ---- rotary frequencies ------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("R,base", [(2, 10000.0), (64, 10000.0), (128, 500000.0), (20, 1e6)])
+def test_plain_frequencies(R, base):
+    freqs, factor = kvq.kvq_rope_frequencies(R, base)
+    assert factor == 1.0 and freqs.shape == (R // 2,)
+    for i, f in enumerate(freqs.tolist()):
+        want = base ** (-2.0 * i / R) / (2 * math.pi)
+        # a handful of float64 roundings, and at most one unit of 2^-64 turns of truncation
+        assert abs(f / 2.0 ** 64 - want) <= 8 * 2.0 ** -53 * want + 2.0 ** -64
+
+
+def test_scaled_frequencies():
+    R, base, n, s = 128, 500000.0, 8192, 8.0
+    plain = np.array([base ** (-2.0 * i / R) for i in range(R // 2)])
+
+    # besides float64 roundings, the frequencies are cut to whole units of 2^-64 turns = 2 pi 2^-64 = 3.41e-19 radians
+    close = lambda x, y: np.testing.assert_allclose(x, y, rtol=1e-14, atol=3.5e-19)  # noqa: E731
+
+    def got(**kw):
+        freqs, factor = kvq.kvq_rope_frequencies(R, base, factor=s, original=n, **kw)
+        return np.array([f / 2.0 ** 64 for f in freqs.tolist()]) * 2 * math.pi, factor
+
+    f, factor = got(scaling="linear")
+    close(f, plain / s)
+    assert factor == 1.0
+    f, factor = got(scaling="bands")
+    turns = n * plain / (2 * math.pi)
+    close(f[turns >= 4], plain[turns >= 4])
+    close(f[turns <= 1], plain[turns <= 1] / s)
+    mid = (turns > 1) & (turns < 4)
+    assert mid.any() and np.all(f[mid] < plain[mid]) and np.all(f[mid] > plain[mid] / s) and factor == 1.0
+    f, factor = got(scaling="yarn")
+    assert factor == pytest.approx(0.1 * math.log(s) + 1.0, rel=2.0 ** -23)
+    close(f[turns >= 40], plain[turns >= 40])
+    close(f[turns <= 0.8], plain[turns <= 0.8] / s)
+    assert np.all(np.diff(f) < 0)
+    f, _ = got(scaling="bands", low=2.0, high=3.0)
+    close(f[turns >= 3], plain[turns >= 3])
+
+
+def test_frequencies_refusals():
+    sc = lambda *a: ctypes.byref(kvq.RopeScaling(*a))  # noqa: E731
+    buf, attn = (ctypes.c_uint64 * 64)(), ctypes.c_float()
+    call = lambda R, base, s, f=buf, a=None: kvq.lib().kvq_rope_frequencies(  # noqa: E731
+        R, base, s, f, ctypes.byref(attn) if a is None else None)
+    assert call(64, 1e4, None) == OK
+    for R in (0, 3, -2):
+        assert call(R, 1e4, None) == BAD
+    for base in (1.0, 0.0, -3.0, math.inf, math.nan):
+        assert call(64, base, None) == BAD
+    assert call(64, 1e4, None, None) == BAD and call(64, 1e4, None, buf, 1) == BAD
+    assert call(64, 1e4, sc(9, 2.0, 8192, 0, 0)) == BAD
+    for factor in (0.5, math.inf, math.nan):
+        assert call(64, 1e4, sc(1, factor, 0, 0, 0)) == BAD
+    for n, low, high in ((0, 0, 0), (-1, 0, 0), (8192, 4, 1), (8192, 2, 2), (8192, -1, 4), (8192, 1, math.inf)):
+        assert call(64, 1e4, sc(2, 2.0, n, low, high)) == BAD
+    assert call(64, 1e4, sc(3, 2.0, 8192, 0.0, 32.0)) == BAD  # yarn: the pair of 0 turns does not exist
+    with pytest.raises(ValueError):
+        kvq.kvq_rope_frequencies(64, scaling="other")
+
+
+# ---- the oracle against independent forms ------------------------------------------------------
+
+
+def test_oracle_angles_are_exact():
+    freqs, _ = kvq.kvq_rope_frequencies(8, 10000.0)
+    pos = [0, 1, 1000003, 2 ** 31 - 1]
+    a = paged_kv.angles(pos, freqs.tolist())
+    for i, p in enumerate(pos):
+        for j, f in enumerate(freqs.tolist()):
+            turn = Fraction(p * f, 1 << 64) % 1
+            turn = turn - 1 if turn > Fraction(1, 2) else turn
+            assert abs(a[i, j] - 2 * math.pi * float(turn)) <= 4e-15
+
+
+def test_oracle_rotation_keeps_norms_and_relative_positions():
+    rng = np.random.default_rng(1)
+    freqs = kvq.kvq_rope_frequencies(16, 10000.0)[0].tolist()
+    q, k = rng.standard_normal((2, 1, 1, 24))
+    for inter in (False, True):
+        dots = []
+        for shift in (0, 7, 100000):
+            a, _ = paged_kv.rotate(q, [5 + shift], freqs, inter, 1.0)
+            b, _ = paged_kv.rotate(k, [2 + shift], freqs, inter, 1.0)
+            assert np.linalg.norm(a) == pytest.approx(np.linalg.norm(q), rel=1e-12)
+            dots.append((a * b).sum())
+        assert np.allclose(dots, dots[0], rtol=0, atol=1e-10)
+
+
+def test_oracle_e4m3_is_torchs_cast():
+    x = torch.randn(20000, generator=torch.Generator().manual_seed(2)) * torch.logspace(-4, 2, 20000)
+    want = x.clamp(-448, 448).to(torch.float8_e4m3fn).to(torch.float64)
+    assert np.array_equal(paged_kv.e4m3(x.double().numpy()), want.numpy())
+
+
+def test_oracle_decode_is_softmax_attention():
+    g = torch.Generator().manual_seed(3)
+    q = torch.randn((1, 4, 8), generator=g, dtype=torch.float64)
+    k, v = (torch.randn((3, 16, 2, 8), generator=g, dtype=torch.float64) for _ in range(2))
+    table, L = np.array([[2, 0, 1]]), 41
+    out, lse, _ = paged_kv.decode(q.numpy(), k.numpy(), v.numpy(), table, [L], 0.3)
+    kk, vv = (x[table[0]].flatten(0, 1)[:L].transpose(0, 1).repeat_interleave(2, 0) for x in (k, v))
+    want = torch.nn.functional.scaled_dot_product_attention(q[0][:, None], kk, vv, scale=0.3)[:, 0]
+    np.testing.assert_allclose(out[0], want.numpy(), atol=1e-12)
+    np.testing.assert_allclose(lse[0], torch.logsumexp((q[0][:, None] @ kk.transpose(1, 2))[:, 0] * 0.3, 1).numpy(), atol=1e-12)
+
+
+# ---- refusals ----------------------------------------------------------------------------------
+
+
+def _plan(**kw):
+    a = dict(ctx=16, ql=16, rows=16, table=16, mb=4, nrows=8, free=16, nfree=9, cur=16, cout=32, seq=64, qsl=64, pos=64,
+             slots=64, batch=128, B=2, T=5, bs=16, nb=10, stream=None)
+    a.update(kw)
+    return kvq.lib().kvq_plan_step(*a.values())
+
+
+def test_plan_step_refusals():
+    for kw in (dict(B=-1), dict(T=-1), dict(mb=-1), dict(nrows=-1), dict(nfree=-1), dict(bs=0), dict(nb=0),
+               dict(ctx=None), dict(table=None), dict(mb=0), dict(nrows=0), dict(rows=None, nrows=1), dict(free=None),
+               dict(cur=None), dict(cout=None), dict(ctx=18), dict(ql=18), dict(rows=18), dict(table=18), dict(free=18),
+               dict(cur=20), dict(cout=20), dict(seq=18), dict(qsl=18), dict(pos=18), dict(slots=20), dict(batch=18),
+               dict(batch=16), dict(seq=16)):
+        assert _plan(**kw) == BAD, kw
+    assert _plan(B=8193) == UNSUP
+    assert _plan(mb=1 << 20, bs=1 << 12) == UNSUP  # lengths past int32
+
+
+def _rot(**kw):
+    a = dict(positions=16, freqs=16, rotary_dim=64, interleaved=0, attn_factor=1.0)
+    a.update(kw)
+    return ctypes.byref(kvq.Rotary(*a.values()))
+
+
+def _rope(**kw):
+    a = dict(q=16, qt=512, qh=64, qo=4096, qot=512, qoh=64, Hq=8, k=16, kt=128, kh=64, ko=8192, kot=128, koh=64, Hk=2,
+             rot=_rot(), dtype=0, T=4, D=64, stream=None)
+    a.update(kw)
+    return kvq.lib().kvq_rope(*a.values())
+
+
+def test_rope_refusals():
+    assert _rope(T=0) == OK and _rope(Hq=0, Hk=0) == OK
+    for kw in (dict(T=-1), dict(Hq=-1), dict(Hk=-1), dict(D=0), dict(dtype=3), dict(dtype=9), dict(rot=None),
+               dict(q=None), dict(qo=None), dict(k=None), dict(ko=None), dict(q=17), dict(ko=17), dict(dtype=2, q=18),
+               dict(qo=16, qot=520), dict(ko=16, koh=72)):
+        assert _rope(**kw) == BAD, kw
+    for kw in (dict(rotary_dim=0), dict(rotary_dim=3), dict(rotary_dim=66), dict(positions=None), dict(freqs=None),
+               dict(positions=18), dict(freqs=20), dict(attn_factor=math.inf), dict(attn_factor=math.nan)):
+        assert _rope(rot=_rot(**kw)) == BAD, kw
+    assert _rope(D=1025) == UNSUP and _rope(Hq=70000) == UNSUP
+
+
+def _kv(**kw):
+    a = dict(k=16, v=16, kb=2048, kt=128, kh=64, vb=2048, vt=128, vh=64, ks=None, vs=None, dtype=0, bs=16, nb=10)
+    a.update(kw)
+    return ctypes.byref(kvq.PagedKv(*a.values()))
+
+
+BAD_CACHES = (dict(k=None), dict(v=None), dict(k=24), dict(v=24), dict(kb=2052), dict(kt=-128), dict(vh=4), dict(bs=0),
+              dict(nb=0), dict(dtype=2), dict(dtype=7), dict(dtype=1), dict(ks=16), dict(vs=16),
+              dict(dtype=3, kt=136), dict(dtype=3, ks=18))
+
+
+def _write(**kw):
+    a = dict(key=16, kt=128, kh=64, value=16, vt=128, vh=64, cache=_kv(), slots=16, q=16, qt=512, qh=64, qo=4096, qot=512,
+             qoh=64, Hq=8, rot=_rot(), dtype=0, T=4, Hk=2, D=64, stream=None)
+    a.update(kw)
+    return kvq.lib().kvq_write_kv(*a.values())
+
+
+def test_write_kv_refusals():
+    assert _write(T=0) == OK
+    for kw in (dict(T=-1), dict(Hq=-1), dict(Hk=0), dict(D=0), dict(dtype=2), dict(dtype=3), dict(cache=None), dict(q=None),
+               dict(qo=None), dict(Hq=0), dict(rot=None), dict(key=None), dict(value=None), dict(slots=None),
+               dict(slots=20), dict(key=24), dict(vt=129), dict(qoh=4), dict(qo=16, qot=520), dict(rot=_rot(rotary_dim=66))):
+        assert _write(**kw) == BAD, kw
+    for kw in BAD_CACHES:
+        assert _write(cache=_kv(**kw)) == BAD, kw
+    assert _write(D=68) == UNSUP and _write(D=264) == UNSUP
+
+
+def _decode(mods=None, **kw):
+    a = dict(q=16, qd=0, cache=_kv(), table=16, mb=4, lens=16, scale=0.1, S=4, ws=16, wsb=1 << 30, out=16, od=2, B=2, Hq=4,
+             Hk=2, D=64, mods=None if mods is None else ctypes.byref(mods), stream=None)
+    a.update(kw)
+    return kvq.lib().kvq_decode_kv(*a.values())
+
+
+def test_decode_kv_refusals():
+    assert _decode(B=0) == OK
+    for kw in (dict(B=-1), dict(Hq=0), dict(Hk=0), dict(Hq=5), dict(mb=-1), dict(mb=0), dict(S=-1), dict(cache=None),
+               dict(qd=2), dict(qd=3), dict(od=3), dict(od=9), dict(scale=0.0), dict(scale=-1.0), dict(scale=math.inf),
+               dict(scale=math.nan), dict(q=None), dict(table=None), dict(lens=None), dict(out=None), dict(ws=None),
+               dict(q=24), dict(table=18), dict(lens=18), dict(out=24), dict(ws=24), dict(qd=1)):
+        assert _decode(**kw) == BAD, kw
+    for kw in BAD_CACHES:
+        assert _decode(cache=_kv(**kw)) == BAD, kw
+    M = kvq.ScoreMods
+    for m in (M(-1, 0.0), M(0, -1.0), M(0, math.inf), M(0, math.nan), M(0, 0.0, 18), M(0, 0.0, None, 18),
+              M(0, 0.0, None, None, -1), M(0, 0.0, None, None, 1, 18)):
+        assert _decode(m) == BAD
+    assert _decode(M(0, 0.0, None, None, 2)) == UNSUP  # several tokens of a sequence
+    assert _decode(M(0, 0.0, None, None, 1, None, 16, 4)) == UNSUP
+    assert _decode(D=80) == UNSUP and _decode(cache=_kv(bs=24)) == UNSUP
+    assert _decode(mb=1 << 27) == UNSUP  # lengths past int32
+    assert _decode(wsb=64) == kvq.KVQ_ERR_WORKSPACE
+
+
+def test_decode_kv_workspace_sizes():
+    r256 = lambda x: (x + 255) // 256 * 256  # noqa: E731
+    # fixed splits: B * S slots, 4 / (kv heads of a CTA) warps a head, a row of D + 1 words for each query head
+    rows = 2 * 4 * 2 * 4
+    assert kvq.kvq_decode_kv_workspace_bytes(2, 4, 2, 64, 4) >= r256(rows * 64 * 4) + r256(rows * 4)
+    assert kvq.kvq_decode_kv_workspace_bytes(2, 5, 2, 64, 4) == 0
+    assert kvq.kvq_decode_kv_workspace_bytes(2, 4, 2, 96, 4) == 0
+    assert kvq.kvq_decode_kv_workspace_bytes(-1, 4, 2, 64, 4) == 0
+    assert kvq.kvq_decode_kv_workspace_bytes(2, 4, 2, 64, -1) == 0
+
+
+def test_binding_refuses_cpu_tensors_and_wrong_types():
+    x = torch.zeros((2, 4, 64), dtype=torch.bfloat16)
+    i = torch.zeros(2, dtype=torch.int32)
+    c = torch.zeros((4, 16, 2, 64), dtype=torch.bfloat16)
+    with pytest.raises(TypeError):
+        kvq.kvq_decode_kv(x, c, c, i[None], i, 0.1)
+    with pytest.raises(TypeError):
+        kvq.kvq_decode_kv(x.float(), c, c, i[None], i, 0.1)
+    with pytest.raises(TypeError):
+        kvq.kvq_rope(x, None, i, i.long())
+    with pytest.raises(TypeError):
+        kvq.kvq_write_kv(x, x, c, c, i.long())
+    with pytest.raises(TypeError):
+        kvq.kvq_plan_step(i, i, i[None], None, None, 16, 4, T=2)
