@@ -183,6 +183,24 @@ bool tq_tensor_map(const void *cache, long long num_blocks, int Hk, int slot_byt
   return true;
 }
 
+bool paged_tensor_map(const void *base, int row_bytes, int part_bytes, int box_heads, long long token, long long head, long long block,
+                      int block_size, int Hk, long long num_blocks, CUtensorMap *map) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = encode_tiled();
+  if (enc == nullptr) return false;
+  const int parts = row_bytes / part_bytes;
+  const cuuint64_t dim[5] = {static_cast<cuuint64_t>(part_bytes), static_cast<cuuint64_t>(block_size),
+                             static_cast<cuuint64_t>(parts), static_cast<cuuint64_t>(Hk), static_cast<cuuint64_t>(num_blocks)};
+  // a dimension of one element may come with any stride, 0 among them: its value plays no part
+  const cuuint64_t stride[4] = {static_cast<cuuint64_t>(token), static_cast<cuuint64_t>(part_bytes),
+                                static_cast<cuuint64_t>(Hk > 1 ? head : row_bytes),
+                                static_cast<cuuint64_t>(num_blocks > 1 ? block : row_bytes)};
+  const cuuint32_t box[5] = {static_cast<cuuint32_t>(part_bytes), 16, static_cast<cuuint32_t>(parts), static_cast<cuuint32_t>(box_heads), 1};
+  const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<void *>(base), dim, stride, box, ones,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, part_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 size_t workspace_bytes(int B, int Hq, int D, const SplitPlan &plan) {
   const size_t rows = static_cast<size_t>(plan.slots) * plan.warps_per_head * Hq;
   return round256(rows * D * sizeof(float)) + round256(rows * sizeof(float)) +

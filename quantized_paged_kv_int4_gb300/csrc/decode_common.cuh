@@ -208,16 +208,15 @@ __device__ __forceinline__ void store_out(const SplitArgs &a, long long row, int
 }
 
 // Merge the partials of (b, hq) in slots [s_lo, s_hi) and write the output row (one warp).
-// Up to 16 partial rows (D = 256: 8) per round trip: their log-sum-exps and their vectors are all requested
+// Up to 16 partial rows per round trip: their log-sum-exps and their vectors are all requested
 // before any is used, then combined online (running max M, weights 2^(lse - M)). Partials come
 // from the split kernel's CTAs: read through L2 (ld.global.cg). sg: this lane's rotation signs
 // (used when a.signs is set); sink2: the head's sink logit in base 2 (-inf: none), a partial with
 // lse = sink2 and a zero vector.
-// NAN_LSE: a NaN among the scores makes the row's log-sum-exp NaN (as it makes the row); otherwise -inf.
-template <int D, bool NAN_LSE = false>
+template <int D>
 __device__ __forceinline__ void merge_row(const SplitArgs &a, int b, int hq, long long orow, long long s_lo,
                                           long long s_hi, int lane, const float (&sg)[D / 32], float sink2) {
-  constexpr int V = D / 32, R = V == 8 ? 8 : 16;  // partial rows in flight: at most 64 registers
+  constexpr int V = D / 32, R = 16;
   const int W = a.warps_per_head;
   const long long n = (s_hi - s_lo) * W, r0 = s_lo * W;  // rows (s * W + w) are contiguous
   float o[V];
@@ -232,12 +231,9 @@ __device__ __forceinline__ void merge_row(const SplitArgs &a, int b, int hq, lon
     for (int k = 0; k < R; ++k) {
       if (k < cnt) {
         const float *src = a.part_o + ((r0 + i0 + k) * a.Hq + hq) * D + lane * V;
-        if constexpr (V % 4 == 0) {
-#pragma unroll
-          for (int j = 0; j < V; j += 4) {
-            const float4 x = __ldcg(reinterpret_cast<const float4 *>(src + j));
-            v[k][j] = x.x; v[k][j + 1] = x.y; v[k][j + 2] = x.z; v[k][j + 3] = x.w;
-          }
+        if constexpr (V == 4) {
+          const float4 x = __ldcg(reinterpret_cast<const float4 *>(src));
+          v[k][0] = x.x; v[k][1] = x.y; v[k][2] = x.z; v[k][3] = x.w;
         } else {
           const float2 x = __ldcg(reinterpret_cast<const float2 *>(src));
           v[k][0] = x.x; v[k][1] = x.y;
@@ -281,7 +277,7 @@ __device__ __forceinline__ void merge_row(const SplitArgs &a, int b, int hq, lon
 #pragma unroll
   for (int j = 0; j < V; ++j) o[j] *= inv;
   if (a.lse_out != nullptr && lane == 0)  // ln(sum of e^S) = (M + log2 den) ln 2
-    a.lse_out[orow] = (NAN_LSE ? den != 0.f : den > 0.f) ? (M + log2f(den)) * 0.6931471805599453f : -INFINITY;
+    a.lse_out[orow] = den > 0.f ? (M + log2f(den)) * 0.6931471805599453f : -INFINITY;
   if (a.signs != nullptr) {
     // element e = lane * V + j: stages h < V inside the lane, h = V .. D/2 across lanes
     butterfly_local<V>(o);
@@ -406,7 +402,7 @@ __device__ __forceinline__ long long run_of_page(long long X, long long q, long 
 // partition for B <= 256, else read from seg_first / seg_last), the rotation signs -- is done
 // before griddepcontrol.wait, which holds the kernel until that grid has finished and its writes
 // are visible; after it, one round trip for the partials.
-template <int D, bool NAN_LSE = false>
+template <int D>
 __global__ void __launch_bounds__(256) merge_kernel(const SplitArgs a) {
   constexpr int V = D / 32;
   __shared__ long long s_scan[8];
@@ -471,7 +467,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const SplitArgs a) {
   }
   s_lo = max(0LL, min(s_lo, a.slots));  // never index outside the workspace
   s_hi = max(s_lo, min(s_hi, a.slots));
-  merge_row<D, NAN_LSE>(a, b, hq, orow, s_lo, s_hi, lane, sg, sink2);
+  merge_row<D>(a, b, hq, orow, s_lo, s_hi, lane, sg, sink2);
 }
 
 }  // namespace kvq

@@ -4,28 +4,39 @@
 // Mathematics: for sequence b, query head hq and its kv head, S_n = scale q . k_n over the sequence's
 // keys, one pass with a running reference m: l = sum 2^(S - m), acc = sum 2^(S - m) v_n, both in fp32;
 // o = acc / l and lse = m + log2 l hold for any m, so m moves (and rescales) only when a score passes
-// m + kSlack. Pieces of a sequence are joined by their log-sum-exps (merge_kernel, decode_common.cuh).
+// m + kSlack. Pieces of a sequence are joined by their log-sum-exps: sum_s 2^(lse_s - M) o_s / sum_s 2^(lse_s - M).
 //
 // What bounds it: HBM. A key and a value of D elements serve the Hq / Hk query heads of their kv head
 // with 4 D Hq / Hk operations, two orders of magnitude below the tensor rate.
 //
-// One warp serves one (kv head, block of 8 NT query heads) over a run of 16-token tiles, with nothing
-// shared between warps. Both products are mma.m16n8k16 with the 16 tokens of a tile as rows of the
-// scores (S^T = K Q^T) and as the depth of the output (O^T = V^T P^T): the operand rows come straight
-// from global memory into registers, 16 bytes a lane, because the order of the head dimension inside a
-// k-step and of the output rows inside an m-tile is free as long as both operands agree:
-//   K: lane (g, t) reads rows g and g + 8, chunk c = dims 32 c + 8 t .. + 7 (FP8: 64 c + 16 t .. + 15);
-//      the query fragments are read with the same order;
-//   V: lane (g, t) reads tokens 2t, 2t + 1, 2t + 8, 2t + 9 at the dims of chunk g; a byte permute of two
-//      tokens' words gives the operand's token pairs.
+// Split. A sequence's keys are cut into pages of 16 tokens. A CTA serves HB kv heads over a run of pages:
+//   balanced (num_splits = 0): the pages of the whole batch, concatenated, are cut into equal runs (first ones a
+//     page longer), one for each CTA of a head group; the partials of CTA x and sequence b go to slot x + b;
+//   fixed (num_splits = S): a sequence's pages are cut into S runs, slot b S + s.
+// Its eight worker warps are HB heads x CB blocks of 8 NT query heads x W pages: each takes every W-th page of the run for
+// one (kv head, block) and writes a partial (o, lse) for every sequence piece. A second kernel joins the partials,
+// as many warps for a row as it has partials to read. Where one CTA has a whole sequence (S = 1, or short
+// tables) it joins them itself, and there is one launch.
+//
+// A ninth warp is the producer: it keeps a ring of the CTA full, walking the same pieces on its own, so that the
+// next piece's tiles are on their way while the workers still finish the last one. A ring slot holds K or V of W pages:
+// one TMA box a page, HB heads x 16 rows (whole HBM rows), in parts of at most 128 bytes, swizzled; "full" and
+// "empty" mbarriers say when it has landed and when every worker has used it. (A ring for each worker, filled by its own
+// lane 0 or by a lane of the producer, measured 97 and 125 us for 64 x 4096 FP8 tokens: eight times the copies to start.)
+//
+// Both products are mma.m16n8k16 with the 16 tokens of a tile as rows of the scores (S^T = K Q^T) and as the depth of the
+// output (O^T = V^T P^T); the operands come from the ring by ldmatrix, K as it lies, V transposed:
+//   16 bits: a k-step is 16 dims, an m-tile 16 dims, in order;
+//   FP8: ldmatrix moves pairs of bytes, so lane (g, t) gets dims 4t .. 4t + 3 of K's 16 (the query fragments are read
+//   in the same order) and dims 2g, 2g + 1 of V's 16 for two tokens, which a byte permute pairs up by token.
 // P goes from the score layout to the operand layout by a transposing warp move (movmatrix).
 //
 // Operands. 16-bit caches enter as they are. FP8 codes become fp16, exactly; q becomes fp16 times 2^-k, k
 // for each query head from its largest element, which keeps every bf16 element within 2^-29 of the
 // largest exactly (query_shift, decode_common.cuh). P is fp16 for fp16 and FP8 caches (relative 2^-11 a
 // weight). For bf16 caches it would be bf16 (2^-8), as large as the rounding of the output itself: there P
-// enters as bf16 hi + lo, relative 2^-16, in two products, which for Hq / Hk <= 4 are the two halves of
-// one product's columns.
+// enters as bf16 hi + lo, relative 2^-16, in two products. For Hq / Hk <= 4 the two parts are the two halves
+// of one product's columns, at no cost, for every type.
 
 #include "decode_common.cuh"
 #include "kvq_host.h"
@@ -34,59 +45,74 @@ namespace kvq {
 
 __device__ unsigned g_flags_decode_kv = 0;
 
+constexpr int kDirectPages = 8;
 constexpr float kSlack = 8.f;  // a weight is at most 2^8: fp16 keeps 2^-14 .. 2^8 at full precision
 
 struct KvParams {
-  SplitArgs s;  // max_blocks in 16-token pages
+  SplitArgs s;      // max_blocks in 16-token pages; seg_ctas: grid.x; slots: of one partial for each query head
+  int32_t col_groups;  // CTAs that share a kv head's query heads (more than 8 blocks of them)
+  int32_t slots;       // of the ring
+  int32_t direct;   // every CTA has whole sequences and writes their rows itself
   const void *q;
-  const uint8_t *k, *v;
-  long long k_block, k_token, k_head, v_block, v_token, v_head;  // bytes
+  CUtensorMap k, v;  // {part bytes, block_size, parts, Hk, num_blocks}, box {part bytes, 16, parts, 1, 1}
   const float *k_scale, *v_scale;
   const int32_t *block_table;
   int32_t bt_stride, bs;
   long long num_blocks;
   int32_t q_f16;       // q is fp16 (else bf16)
-  int32_t col_blocks;  // blocks of 8 NT query heads per kv head
+  int32_t col_blocks;  // blocks of 8 NT query heads of a CTA (CB)
   float sc_log2;       // softmax_scale * log2(e)
   float cap2, inv_cap2;  // soft cap in base 2
   const float *alibi;
+  unsigned long long wait_ns;  // limit of every bounded wait on a ring slot
+  int32_t withhold;            // error-path tests only: ring slot `withhold` of CTA (0, 0)'s first worker is never filled
 };
 
 enum : int { KV_BF16 = 0, KV_F16 = 1, KV_E4M3 = 2 };
 
-template <int D, int CT, int NT>
-struct KvGeom {
-  static constexpr int ES = CT == KV_E4M3 ? 1 : 2;
-  static constexpr int ROW = D * ES;               // bytes of a row
-  static constexpr int KC = ROW / 64;              // 16-byte chunks per lane of a K row
-  static constexpr int VB = ROW / 8 < 16 ? ROW / 8 : 16;  // bytes of a lane's V chunk
-  static constexpr int VC = ROW / (8 * VB);        // chunks per lane of a V row
-  static constexpr int MT = D / 16;                // output m-tiles
-  static constexpr int KS = D / 16;                // k-steps
-  // tiles in flight: 8 KB of K and V for each warp
-  static constexpr int U = ROW >= 256 ? 1 : (ROW == 128 ? 2 : 4);
+constexpr int kKvWarps = 8;  // workers of a CTA; one CTA an SM: the ring fills the shared memory
+constexpr int kKvMaxSlots = 16;
+constexpr int kKvThreads = 32 * (kKvWarps + 1);
+
+template <int D, int CT>
+struct KvGeom {  // HALF: K or V of one (page, kv head)
+  static constexpr int ROW = D * (CT == KV_E4M3 ? 1 : 2);  // bytes of a row
+  static constexpr int PB = ROW < 128 ? ROW : 128;         // bytes of a part
+  static constexpr int HALF = kPage * ROW;                 // K (or V) of a tile
+  static constexpr int MT = D / 16;                        // output m-tiles, and k-steps of the scores
+  static constexpr int RING = 216 * 1024;                  // bytes of the ring
 };
 
-__device__ __forceinline__ uint4 ldg_stream16(const uint8_t *p) {
-  uint4 r;
-  asm volatile("ld.global.nc.L1::no_allocate.L2::128B.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-               : "l"(p));
-  return r;
+__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
 }
-__device__ __forceinline__ uint2 ldg_stream8(const uint8_t *p) {
-  uint2 r;
-  asm volatile("ld.global.nc.L1::no_allocate.L2::128B.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
-  return r;
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, int c3, int c4,
+                                            uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, "
+      "%4, %5, %6}], [%7];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(bar)
+      : "memory");
 }
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
   uint32_t y;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t two) {
-  const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3);
-  return static_cast<uint32_t>(r.x) | (static_cast<uint32_t>(r.y) << 16);
+// four E4M3FN codes -> fp16: the low two in lo, the high two in hi (exact; a NaN stays a NaN)
+__device__ __forceinline__ void e4m3x4_f16x4(uint32_t x, uint32_t &lo, uint32_t &hi) {
+  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(x));
 }
 template <int CT>
 __device__ __forceinline__ void mma_kv(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -99,31 +125,77 @@ __device__ __forceinline__ void mma_kv(float (&c)[4], uint32_t a0, uint32_t a1, 
     mma_f16_16816(c, a0, a1, a2, a3, b0, b1);
 }
 __device__ __forceinline__ uint32_t bf2_as_u32(__nv_bfloat162 b) { return *reinterpret_cast<uint32_t *>(&b); }
-__device__ __forceinline__ uint32_t word(const uint4 &r, int i) { return i == 0 ? r.x : i == 1 ? r.y : i == 2 ? r.z : r.w; }
 
-// One warp, one piece [t0, t1) of sequence b: kv head h, query heads h G + 8 NT cb .. of it; the warp takes
-// every warps_per_head-th tile. FOLD (bf16, G <= 4): columns 4 .. 7 repeat the heads of columns 0 .. 3 and
-// take the low parts of P.
+// The pieces of a CTA's run.
+struct KvPiece {
+  int b, page, n, L, lo;  // pages page .. page + n - 1 of sequence b; live keys are [lo, L)
+  long long slot;
+};
+struct KvCursor {
+  long long P, pb, pe;  // first page (concatenated) of sequence b, the run
+  int b;
+};
+__device__ __forceinline__ bool next_piece(const SplitArgs &a, KvCursor &c, KvPiece &pc) {
+  if (a.num_splits > 0) {
+    const int b = c.b, s = static_cast<int>(blockIdx.x) % a.num_splits;
+    if (b < 0) return false;
+    c.b = -1;
+    const SeqSpan sp = seq_span(a, b, nullptr);
+    const int per = (sp.np + a.num_splits - 1) / a.num_splits;
+    const long long lo = static_cast<long long>(s) * per, left = sp.np - lo;
+    pc = {b, sp.f + static_cast<int>(lo), static_cast<int>(min(static_cast<long long>(per), left)), sp.L, sp.lo,
+          static_cast<long long>(blockIdx.x)};
+    return left > 0;
+  }
+  while (c.P < c.pe && c.b < a.B) {
+    const int b = c.b++;
+    const SeqSpan sp = seq_span(a, b, nullptr);
+    const long long P = c.P;
+    c.P += sp.np;
+    if (sp.np > 0) {
+      const int lo = static_cast<int>(max(c.pb, P) - P), hi = static_cast<int>(min(c.pe, P + sp.np) - P);
+      pc = {b, sp.f + lo, hi - lo, sp.L, sp.lo, static_cast<long long>(blockIdx.x) + b};
+      return true;
+    }
+  }
+  return false;
+}
+
+// The ring: the slot and phase that come next.
+struct KvRing {
+  uint32_t addr, full, empty;  // shared-window addresses of slot 0 (a worker: its own tile there) and of the barriers
+  uint32_t stride;             // bytes of a slot
+  uint32_t n, at, phase;
+  __device__ __forceinline__ void advance() {
+    at = at + 1 == n ? 0 : at + 1;
+    phase ^= at == 0;
+  }
+};
+
+// One worker, one piece: kv head h, query heads h G + 8 NT cb .. of it, pages sub, sub + W, ... of the piece. FOLD (G <= 4): columns 4 .. 7 repeat the
+// heads of columns 0 .. 3 and take the low parts of P. False when a wait on the ring ran out.
 template <int D, int CT, int NT, bool FOLD, bool MODS>
-__device__ __forceinline__ void kv_piece(const KvParams &p, int b, int h, int cb, int sub, int t0, int t1, int L,
-                                         long long slot) {
-  using Gm = KvGeom<D, CT, NT>;
-  constexpr int U = Gm::U;
+__device__ __forceinline__ bool kv_piece(const KvParams &p, KvRing &rg, uint8_t *ring, const uint8_t *bad, int h, int cb,
+                                         int sub, const KvPiece &pc) {
+  using Gm = KvGeom<D, CT>;
+  constexpr int MT = Gm::MT;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int G = p.s.G, WPH = p.s.warps_per_head, c0 = cb * 8 * NT;  // first query head of the block
-
-  const int first = t0 / kPage + sub, last = (t1 - 1) / kPage;
-  const int n_my = first <= last ? (last - first) / WPH + 1 : 0;
-  const int32_t *bt = p.block_table + static_cast<long long>(b) * p.bt_stride;
-  const int tpb = p.bs / kPage;  // tiles of a block
-  auto load_ids = [&](int batch) -> int {
-    const int i = batch * 32 + lane;
-    return i < n_my ? __ldg(bt + (first + i * WPH) / tpb) : -1;
+  const int G = p.s.G, c0 = cb * 8 * NT;  // first query head of the block
+  const int b = pc.b, W = p.s.warps_per_head;
+  auto landed = [&]() -> bool {  // the ring's next entry
+    const uint32_t bar = rg.full + 8 * rg.at;
+    if (__all_sync(FULL, mbar_try_wait(bar, rg.phase)) || __all_sync(FULL, mbar_wait(bar, rg.phase, p.wait_ns))) return true;
+    if (lane == 0) atomicOr(&g_flags_decode_kv, ERR_TIMEOUT);
+    return false;
   };
-  int ids = load_ids(0), ids_next = load_ids(1), batch = 0;
+  auto release = [&]() {  // the warp has used the entry
+    __syncwarp();
+    if (lane == 0) mbar_arrive(rg.empty + 8 * rg.at);
+    rg.advance();
+  };
 
   // the query fragments, b0 / b1 of k-step ks
-  uint32_t qf[NT][Gm::KS][2];
+  uint32_t qf[NT][MT][2];
   float sc[NT][2];   // score scale of columns 2t, 2t + 1
   float slope[NT][2];
   const float k_scale = CT == KV_E4M3 && p.k_scale != nullptr ? __ldg(p.k_scale + h) : 1.f;
@@ -131,48 +203,44 @@ __device__ __forceinline__ void kv_piece(const KvParams &p, int b, int h, int cb
   for (int nt = 0; nt < NT; ++nt) {
     const int col = FOLD ? (g & 3) : c0 + 8 * nt + g;
     const bool live = col < G;
-    const uint8_t *qr = static_cast<const uint8_t *>(p.q) +
-                        (static_cast<long long>(b) * p.s.Hq + static_cast<long long>(h) * G + (live ? col : 0)) * D * 2;
+    const uint32_t *qr = static_cast<const uint32_t *>(p.q) +
+                         (static_cast<long long>(b) * p.s.Hq + static_cast<long long>(h) * G + (live ? col : 0)) * (D / 2);
     if constexpr (CT != KV_E4M3) {
 #pragma unroll
-      for (int c = 0; c < Gm::KC; ++c) {
-        const uint4 r = live ? __ldg(reinterpret_cast<const uint4 *>(qr + 64 * c + 16 * t)) : make_uint4(0, 0, 0, 0);
-        qf[nt][2 * c][0] = r.x;
-        qf[nt][2 * c][1] = r.y;
-        qf[nt][2 * c + 1][0] = r.z;
-        qf[nt][2 * c + 1][1] = r.w;
+      for (int ks = 0; ks < MT; ++ks) {
+        qf[nt][ks][0] = live ? __ldg(qr + 8 * ks + t) : 0u;
+        qf[nt][ks][1] = live ? __ldg(qr + 8 * ks + 4 + t) : 0u;
       }
       sc[nt][0] = sc[nt][1] = p.sc_log2;
     } else {
-      uint32_t w[2 * Gm::KS];  // element pairs: chunk c's 16 dims are words 8 c .. 8 c + 7
       float big = 0.f;
-#pragma unroll
-      for (int c = 0; c < Gm::KC; ++c) {
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          const uint4 r = live ? __ldg(reinterpret_cast<const uint4 *>(qr + 128 * c + 32 * t + 16 * hf)) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) w[8 * c + 4 * hf + i] = word(r, i);
-        }
-      }
       auto pair = [&](uint32_t x) {
         return p.q_f16 ? __half22float2(u32_as_h2(x))
                        : make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
       };
 #pragma unroll
-      for (int i = 0; i < 2 * Gm::KS; ++i) {
-        const float2 f = pair(w[i]);
-        big = fmaxf(big, fmaxf(fabsf(f.x), fabsf(f.y)));
+      for (int ks = 0; ks < MT; ++ks) {
+        const uint2 r = live ? __ldg(reinterpret_cast<const uint2 *>(qr + 8 * ks + 2 * t)) : make_uint2(0u, 0u);
+        qf[nt][ks][0] = r.x;
+        qf[nt][ks][1] = r.y;
+      }
+#pragma unroll
+      for (int ks = 0; ks < MT; ++ks) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float2 f = pair(qf[nt][ks][i]);
+          big = fmaxf(big, fmaxf(fabsf(f.x), fabsf(f.y)));
+        }
       }
       big = fmaxf(big, __shfl_xor_sync(FULL, big, 1));
       big = fmaxf(big, __shfl_xor_sync(FULL, big, 2));
       const int k = query_shift(big, 0, live ? &g_flags_decode_kv : nullptr);
       const float down = pow2i(-k), up = pow2i(k) * p.sc_log2 * k_scale;
 #pragma unroll
-      for (int ks = 0; ks < Gm::KS; ++ks) {
+      for (int ks = 0; ks < MT; ++ks) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float2 f = pair(w[2 * ks + i]);
+          const float2 f = pair(qf[nt][ks][i]);
           qf[nt][ks][i] = h2_as_u32(__floats2half2_rn(f.x * down, f.y * down));
         }
       }
@@ -188,378 +256,544 @@ __device__ __forceinline__ void kv_piece(const KvParams &p, int b, int h, int cb
     }
   }
 
-  float m[NT][2], l[NT][2], acc[NT][Gm::MT][4];
+  float m[NT][2], l[NT][2], acc[NT][MT][4];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     m[nt][0] = m[nt][1] = -INFINITY;
     l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
-    for (int i = 0; i < Gm::MT; ++i) acc[nt][i][0] = acc[nt][i][1] = acc[nt][i][2] = acc[nt][i][3] = 0.f;
+    for (int i = 0; i < MT; ++i) acc[nt][i][0] = acc[nt][i][1] = acc[nt][i][2] = acc[nt][i][3] = 0.f;
   }
 
-  const uint8_t *kh = p.k + h * p.k_head + g * p.k_token + 16 * t;
-  const uint8_t *vh = p.v + h * p.v_head + 2 * t * p.v_token + Gm::VB * g;
-  // Tile i of the warp: its block and its place in it. A tile past the end or in a bad block gives an
-  // offset inside the pool (block 0) and no live tokens.
-  struct Tile {
-    long long blk;
-    int row, pos, lo, hi;  // live tokens [lo, hi) of the tile
+  // ldmatrix: lane l gives the row of matrix l / 8. K: matrices (tokens 0-7, chunk c), (8-15, c), (0-7, c + 1),
+  // (8-15, c + 1); V: (tokens 0-7, c), (0-7, c + 1), (8-15, c), (8-15, c + 1). Chunk c of a row lies at c ^ (row % 8)
+  // (parts of 128 bytes) or c ^ (row / 2 % 4) (64 bytes).
+  constexpr int CP = Gm::PB / 16;  // chunks of a part
+  const int mrow = lane & 7, msel = lane >> 3;
+  const uint32_t swz_x = Gm::PB == 128 ? mrow : (mrow >> 1);
+  const uint32_t k_lane = (mrow + 8 * (msel & 1)) * Gm::PB + (((msel >> 1) ^ swz_x) << 4);
+  const uint32_t v_lane = (mrow + 8 * (msel >> 1)) * Gm::PB + (((msel & 1) ^ swz_x) << 4);
+  // chunk 2 c2 + (the lane's 0 or 1) of the lane's row, base = slot + k_lane or v_lane: slots are 1024-byte aligned, so
+  // the chunk's bits are the address's
+  auto chunk_at = [&](uint32_t base, int c2) -> uint32_t {
+    return (base ^ ((2 * c2 % CP) << 4)) + (2 * c2 / CP) * (kPage * Gm::PB);
   };
-  auto tile_of = [&](int i) -> Tile {
-    if (i < n_my && (i >> 5) != batch) {  // warp-uniform
-      batch = i >> 5;
-      ids = ids_next;
-      ids_next = load_ids(batch + 1);
-    }
-    const int id = __shfl_sync(FULL, ids, i & 31);
-    Tile x;
-    const int page = first + i * WPH;
-    x.pos = page * kPage;
-    const bool in = i < n_my, ok = in && id >= 0 && id < p.num_blocks;
-    if (in && !ok && lane == 0) atomicOr(&g_flags_decode_kv, ERR_BLOCK);
-    x.blk = ok ? id : 0;
-    x.row = ok ? (page % tpb) * kPage : 0;
-    x.lo = ok ? max(t0 - x.pos, 0) : 0;
-    x.hi = ok ? min(t1 - x.pos, kPage) : 0;
-    return x;
-  };
-  uint4 kr[U][2][Gm::KC];
-  Tile tile[U], next[U];
-  auto load_k = [&](const Tile &x, uint4 (&r)[2][Gm::KC]) {
-    const uint8_t *src = kh + x.blk * p.k_block + x.row * p.k_token;
-#pragma unroll
-    for (int c = 0; c < Gm::KC; ++c) {
-      r[0][c] = ldg_stream16(src + 64 * c);
-      r[1][c] = ldg_stream16(src + 8 * p.k_token + 64 * c);
-    }
-  };
-  if (n_my > 0) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      tile[u] = tile_of(u);
-      load_k(tile[u], kr[u]);
-    }
-  }
 
-  for (int i0 = 0; i0 < n_my; i0 += U) {
-    // ---- values of this step on their way
-    uint32_t vr[U][4][Gm::VC * Gm::VB / 4];
+  for (int i = sub; i - sub < pc.n; i += W) {
+    if (!landed()) return false;
+    if (i >= pc.n) {  // the run ends inside the slot: nothing of this worker's
+      release();
+      if (!landed()) return false;
+      release();
+      break;
+    }
+    const uint32_t ka = rg.addr + rg.at * rg.stride + k_lane;
+    const int pos = (pc.page + i) * kPage;
+    const bool dead = (bad[rg.at] >> sub & 1) != 0;  // no block of its own
+    const int lo = max(pc.lo - pos, 0), hi = dead ? 0 : min(pc.L - pos, kPage);  // live tokens of the tile
+    const bool partial = lo > 0 || hi < kPage;  // warp-uniform
+    // ---- scores: rows are tokens g, g + 8, columns 2t, 2t + 1; two chains of products
+    float S[2][NT][4];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const uint8_t *src = vh + tile[u].blk * p.v_block + tile[u].row * p.v_token;
+    for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint8_t *r = src + ((j & 1) + 8 * (j >> 1)) * p.v_token;
+      for (int e = 0; e < 4; ++e) S[0][nt][e] = S[1][nt][e] = 0.f;
+    }
+    if constexpr (CT != KV_E4M3) {
 #pragma unroll
-        for (int c = 0; c < Gm::VC; ++c) {
-          if constexpr (Gm::VB == 16) {
-            const uint4 x = ldg_stream16(r + 128 * c);
-            vr[u][j][4 * c] = x.x;
-            vr[u][j][4 * c + 1] = x.y;
-            vr[u][j][4 * c + 2] = x.z;
-            vr[u][j][4 * c + 3] = x.w;
-          } else {
-            const uint2 x = ldg_stream8(r);
-            vr[u][j][0] = x.x;
-            vr[u][j][1] = x.y;
-          }
+      for (int ks = 0; ks < MT; ++ks) {
+        uint32_t a[4];
+        ldmatrix4(chunk_at(ka, ks), a);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma_kv<CT>(S[ks & 1][nt], a[0], a[1], a[2], a[3], qf[nt][ks][0], qf[nt][ks][1]);
+      }
+    } else {
+#pragma unroll
+      for (int k2 = 0; k2 < MT / 2; ++k2) {
+        uint32_t r[4];
+        ldmatrix4(chunk_at(ka, k2), r);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          uint32_t a0, a1, a2, a3;
+          e4m3x4_f16x4(r[2 * u], a0, a2);
+          e4m3x4_f16x4(r[2 * u + 1], a1, a3);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma_kv<CT>(S[u][nt], a0, a1, a2, a3, qf[nt][2 * k2 + u][0], qf[nt][2 * k2 + u][1]);
         }
       }
     }
-    // ---- scores: rows are tokens g, g + 8, columns 2t, 2t + 1
-    float S[U][NT][4];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) S[u][nt][0] = S[u][nt][1] = S[u][nt][2] = S[u][nt][3] = 0.f;
-#pragma unroll
-      for (int c = 0; c < Gm::KC; ++c) {
-        if constexpr (CT != KV_E4M3) {
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma_kv<CT>(S[u][nt], word(kr[u][0][c], 2 * hf), word(kr[u][1][c], 2 * hf), word(kr[u][0][c], 2 * hf + 1),
-                         word(kr[u][1][c], 2 * hf + 1), qf[nt][2 * c + hf][0], qf[nt][2 * c + hf][1]);
-          }
-        } else {
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const uint32_t x = word(kr[u][0][c], w), y = word(kr[u][1][c], w);
-            const uint32_t a0 = e4m3x2_f16x2(x & 0xffffu), a2 = e4m3x2_f16x2(x >> 16);
-            const uint32_t a1 = e4m3x2_f16x2(y & 0xffffu), a3 = e4m3x2_f16x2(y >> 16);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma_kv<CT>(S[u][nt], a0, a1, a2, a3, qf[nt][4 * c + w][0], qf[nt][4 * c + w][1]);
-          }
-        }
-      }
-    }
-    // ---- keys of the next step on their way
-    const bool more = i0 + U < n_my;
-    if (more) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        next[u] = tile_of(i0 + U + u);
-        load_k(next[u], kr[u]);
-      }
-    }
+    release();
     // ---- weights
     bool above = false;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
+    for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float x = S[u][nt][e] * sc[nt][e & 1];
-          if constexpr (MODS) {
-            if (p.cap2 > 0.f) x = p.cap2 * tanhf(x * p.inv_cap2);
-            x = fmaf(slope[nt][e & 1], static_cast<float>(tile[u].pos + g + 8 * (e >> 1) - (L - 1)), x);
-          }
-          const int row = g + 8 * (e >> 1);
-          x = row >= tile[u].lo && row < tile[u].hi ? x : -INFINITY;
-          S[u][nt][e] = x;
-          above |= x > m[nt][e & 1] + kSlack;
+      for (int e = 0; e < 4; ++e) {
+        float x = (S[0][nt][e] + S[1][nt][e]) * sc[nt][e & 1];
+        [[maybe_unused]] const int row = g + 8 * (e >> 1);
+        if constexpr (MODS) {
+          if (p.cap2 > 0.f) x = p.cap2 * tanhf(x * p.inv_cap2);
+          x = fmaf(slope[nt][e & 1], static_cast<float>(pos + row - (pc.L - 1)), x);
         }
+        S[0][nt][e] = x;
       }
     }
-    if (__any_sync(FULL, above)) {  // the references move up to the step's largest scores
+    if (partial) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float top = m[nt][i];
+        for (int e = 0; e < 4; ++e)
+          if (g + 8 * (e >> 1) < lo || g + 8 * (e >> 1) >= hi) S[0][nt][e] = -INFINITY;
+      }
+    }
 #pragma unroll
-          for (int u = 0; u < U; ++u) top = fmaxf(top, fmaxf(S[u][nt][i], S[u][nt][i + 2]));
-          top = warp_max_g(top);
-          const float al = m[nt][i] == top ? 1.f : fast_exp2(m[nt][i] - top);
-          m[nt][i] = top;
-          l[nt][i] *= al;
+    for (int nt = 0; nt < NT; ++nt) above |= fmaxf(S[0][nt][0], S[0][nt][2]) > m[nt][0] + kSlack ||
+                                             fmaxf(S[0][nt][1], S[0][nt][3]) > m[nt][1] + kSlack;
+    if (__any_sync(FULL, above)) {  // the references move up to the tile's largest scores
 #pragma unroll
-          for (int k = 0; k < Gm::MT; ++k) {
-            acc[nt][k][i] *= al;
-            acc[nt][k][i + 2] *= al;
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float top = warp_max_g(fmaxf(m[nt][e], fmaxf(S[0][nt][e], S[0][nt][e + 2])));
+          const float al = m[nt][e] == top ? 1.f : fast_exp2(m[nt][e] - top);
+          m[nt][e] = top;
+          l[nt][e] *= al;
+#pragma unroll
+          for (int k = 0; k < MT; ++k) {
+            acc[nt][k][e] *= al;
+            acc[nt][k][e + 2] *= al;
           }
         }
       }
     }
     // ---- P in operand order: b0 tokens 2t, 2t + 1, b1 tokens 2t + 8, 2t + 9 of column g
-    uint32_t ph[U][NT][2], pl[U][NT][2];
+    uint32_t ph[NT][2], pl[NT][2];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
+    for (int nt = 0; nt < NT; ++nt) {
+      float w[4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float w[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float ref = m[nt][e & 1];
-          w[e] = fast_exp2(S[u][nt][e] - (ref == -INFINITY ? 0.f : ref));
-          l[nt][e & 1] += w[e];
-        }
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          if constexpr (CT == KV_BF16) {
-            const __nv_bfloat162 hi = __floats2bfloat162_rn(w[2 * r], w[2 * r + 1]);
-            const __nv_bfloat162 lo = __floats2bfloat162_rn(w[2 * r] - __low2float(hi), w[2 * r + 1] - __high2float(hi));
-            if constexpr (FOLD) {
-              ph[u][nt][r] = movmatrix_trans(t < 2 ? bf2_as_u32(hi) : bf2_as_u32(lo));
-            } else {
-              ph[u][nt][r] = movmatrix_trans(bf2_as_u32(hi));
-              pl[u][nt][r] = movmatrix_trans(bf2_as_u32(lo));
-            }
-          } else {
-            ph[u][nt][r] = movmatrix_trans(h2_as_u32(__floats2half2_rn(w[2 * r], w[2 * r + 1])));
-          }
-        }
+      for (int e = 0; e < 4; ++e) {
+        const float ref = m[nt][e & 1];
+        w[e] = fast_exp2(S[0][nt][e] - (ref == -INFINITY ? 0.f : ref));
+        l[nt][e & 1] += w[e];
       }
-    }
-    // ---- values of dead tokens may be anything: zero them (0 * NaN is NaN)
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (tile[u].lo > 0 || tile[u].hi < kPage) {  // warp-uniform
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int row = 2 * t + (j & 1) + 8 * (j >> 1);
-          if (row < tile[u].lo || row >= tile[u].hi) {
-#pragma unroll
-            for (int c = 0; c < Gm::VC * Gm::VB / 4; ++c) vr[u][j][c] = 0;
-          }
+      for (int r = 0; r < 2; ++r) {
+        uint32_t hi16, lo16 = 0;
+        if constexpr (CT == KV_BF16) {
+          const __nv_bfloat162 x = __floats2bfloat162_rn(w[2 * r], w[2 * r + 1]);
+          hi16 = bf2_as_u32(x);
+          lo16 = bf2_as_u32(__floats2bfloat162_rn(w[2 * r] - __low2float(x), w[2 * r + 1] - __high2float(x)));
+        } else {
+          const __half2 x = __floats2half2_rn(w[2 * r], w[2 * r + 1]);
+          hi16 = h2_as_u32(x);
+          if constexpr (FOLD) lo16 = h2_as_u32(__floats2half2_rn(w[2 * r] - __low2float(x), w[2 * r + 1] - __high2float(x)));
+        }
+        if constexpr (FOLD) {
+          ph[nt][r] = movmatrix_trans(t < 2 ? hi16 : lo16);
+        } else {
+          ph[nt][r] = movmatrix_trans(hi16);
+          if constexpr (CT == KV_BF16) pl[nt][r] = movmatrix_trans(lo16);
         }
       }
     }
     // ---- O^T += V^T P^T
+    if (!landed()) return false;
+    if (partial) {  // values of dead tokens may be anything: zero them (0 * NaN is NaN)
+      uint8_t *vs = ring + rg.at * rg.stride;
+      for (int c = lane; c < Gm::HALF / 16; c += 32) {
+        const int row = c / CP % kPage;
+        if (row < lo || row >= hi) *reinterpret_cast<uint4 *>(vs + 16 * c) = make_uint4(0, 0, 0, 0);
+      }
+      fence_proxy_async();
+      __syncwarp();
+    }
+    const uint32_t va = rg.addr + rg.at * rg.stride + v_lane;
+    if constexpr (CT != KV_E4M3) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
+      for (int k = 0; k < MT; ++k) {
+        uint32_t a[4];
+        ldmatrix4_trans(chunk_at(va, k), a);
 #pragma unroll
-      for (int c = 0; c < Gm::VC * Gm::VB / 4; ++c) {
-        const uint32_t va = vr[u][0][c], vb = vr[u][1][c], vc = vr[u][2][c], vd = vr[u][3][c];
-        if constexpr (CT != KV_E4M3) {
-          const uint32_t a0 = __byte_perm(va, vb, 0x5410), a1 = __byte_perm(va, vb, 0x7632);
-          const uint32_t a2 = __byte_perm(vc, vd, 0x5410), a3 = __byte_perm(vc, vd, 0x7632);
+        for (int nt = 0; nt < NT; ++nt) {
+          mma_kv<CT>(acc[nt][k], a[0], a[1], a[2], a[3], ph[nt][0], ph[nt][1]);
+          if constexpr (CT == KV_BF16 && !FOLD) mma_kv<CT>(acc[nt][k], a[0], a[1], a[2], a[3], pl[nt][0], pl[nt][1]);
+        }
+      }
+    } else {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma_kv<CT>(acc[nt][c], a0, a1, a2, a3, ph[u][nt][0], ph[u][nt][1]);
-            if constexpr (CT == KV_BF16 && !FOLD) mma_kv<CT>(acc[nt][c], a0, a1, a2, a3, pl[u][nt][0], pl[u][nt][1]);
-          }
-        } else {
+      for (int k2 = 0; k2 < MT / 2; ++k2) {
+        uint32_t r[4];
+        ldmatrix4_trans(chunk_at(va, k2), r);
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {  // dims 4 c + 2 hf, + 1 of the lane's chunk: one m-tile
-            const uint32_t sel = hf ? 0x7362u : 0x5140u;
-            const uint32_t x = __byte_perm(va, vb, sel), y = __byte_perm(vc, vd, sel);
-            const uint32_t a0 = e4m3x2_f16x2(x & 0xffffu), a1 = e4m3x2_f16x2(x >> 16);
-            const uint32_t a2 = e4m3x2_f16x2(y & 0xffffu), a3 = e4m3x2_f16x2(y >> 16);
+        for (int u = 0; u < 2; ++u) {  // dims 16 (2 k2 + u) + 2g, + 1
+          uint32_t a0, a1, a2, a3;
+          e4m3x4_f16x4(__byte_perm(r[u], 0, 0x3120), a0, a1);
+          e4m3x4_f16x4(__byte_perm(r[u + 2], 0, 0x3120), a2, a3);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma_kv<CT>(acc[nt][2 * c + hf], a0, a1, a2, a3, ph[u][nt][0], ph[u][nt][1]);
-          }
+          for (int nt = 0; nt < NT; ++nt) mma_kv<CT>(acc[nt][2 * k2 + u], a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
         }
       }
     }
-    if (more) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) tile[u] = next[u];
-    }
+    release();
   }
 
-  // ---- the piece's partial: column n, dims EPC g' .. of the lane's chunks (two for each m-tile)
-  constexpr int DPL = Gm::VC * Gm::VB / Gm::ES / Gm::VC;  // dims of a chunk
-  const long long row0 = (slot * WPH + sub) * p.s.Hq + static_cast<long long>(h) * G;
+  // ---- the piece's partial: lane (g, t) has columns 2t, 2t + 1 at two dims of each m-tile, 16 k + g and + 8 (FP8:
+  // 16 k + 2g and + 1)
+  const long long row0 = (pc.slot * W + sub) * p.s.Hq + static_cast<long long>(h) * G;
   const float v_scale = CT == KV_E4M3 && p.v_scale != nullptr ? __ldg(p.v_scale + h) : 1.f;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float sum = warp_sum_g(l[nt][i]);
+    for (int e = 0; e < 2; ++e) {
+      const float sum = warp_sum_g(l[nt][e]);
       const float inv = sum > 0.f ? v_scale / sum : (sum == 0.f ? 0.f : sum);  // NaN stays
-      float o[2 * Gm::MT];
+      const int col = c0 + 8 * nt + 2 * t + e;
+      const bool owns = col < G && (!FOLD || t < 2);
+      float *dst = p.s.part_o + (row0 + (owns ? col : 0)) * D;
 #pragma unroll
-      for (int k = 0; k < Gm::MT; ++k) {
-        float x = acc[nt][k][i], y = acc[nt][k][i + 2];
+      for (int k = 0; k < MT; ++k) {
+        float x = acc[nt][k][e], y = acc[nt][k][e + 2];
         if constexpr (FOLD) {
           x += __shfl_xor_sync(FULL, x, 2);
           y += __shfl_xor_sync(FULL, y, 2);
         }
-        o[2 * k] = x * inv;
-        o[2 * k + 1] = y * inv;
+        if (owns) {
+          if constexpr (CT == KV_E4M3) {
+            *reinterpret_cast<float2 *>(dst + 16 * k + 2 * g) = make_float2(x * inv, y * inv);
+          } else {
+            dst[16 * k + g] = x * inv;
+            dst[16 * k + 8 + g] = y * inv;
+          }
+        }
       }
-      const int col = c0 + 8 * nt + 2 * t + i;
-      if (col < G && (!FOLD || t < 2)) {
-        float *dst = p.s.part_o + (row0 + col) * D + DPL * g;
+      if (owns && g == 0) p.s.part_lse[row0 + col] = sum == 0.f ? -INFINITY : m[nt][e] + log2f(sum);
+    }
+  }
+  return true;
+}
+
+// Joins the partials n_lo, n_lo + step, ... < n_hi (slot * W + page of the slot) of row hq into (M, den, o): R of them a round trip, read through L2.
+template <int D>
+__device__ __forceinline__ void kv_join(const SplitArgs &a, int hq, long long n_lo, long long n_hi, int step, int lane, float &M,
+                                        float &den, float (&o)[D / 32]) {
+  constexpr int V = D / 32, R = V == 8 ? 8 : 16;
 #pragma unroll
-        for (int k = 0; k < 2 * Gm::MT; k += 4)
-          *reinterpret_cast<float4 *>(dst + (k / DPL) * 8 * DPL + k % DPL) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
-        if (g == 0) p.s.part_lse[row0 + col] = sum == 0.f ? -INFINITY : m[nt][i] + log2f(sum);
+  for (int j = 0; j < V; ++j) o[j] = 0.f;
+  M = -INFINITY;
+  den = 0.f;
+  for (long long i0 = n_lo; i0 < n_hi; i0 += static_cast<long long>(R) * step) {
+    const long long left = (n_hi - i0 + step - 1) / step;
+    const int cnt = static_cast<int>(min(static_cast<long long>(R), left));
+    const float lse = lane < cnt ? __ldcg(a.part_lse + (i0 + static_cast<long long>(lane) * step) * a.Hq + hq) : -INFINITY;
+    float v[R][V];
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      if (k < cnt) {
+        const float *src = a.part_o + ((i0 + static_cast<long long>(k) * step) * a.Hq + hq) * D + lane * V;
+        if constexpr (V == 2) {
+          const float2 x = __ldcg(reinterpret_cast<const float2 *>(src));
+          v[k][0] = x.x;
+          v[k][1] = x.y;
+        } else {
+#pragma unroll
+          for (int j = 0; j < V; j += 4) {
+            const float4 x = __ldcg(reinterpret_cast<const float4 *>(src + j));
+            v[k][j] = x.x;
+            v[k][j + 1] = x.y;
+            v[k][j + 2] = x.z;
+            v[k][j + 3] = x.w;
+          }
+        }
+      }
+    }
+    const float nM = fmaxf(M, warp_max(lse));
+    if (nM != -INFINITY) {
+      const float f = M == -INFINITY ? 0.f : exp2f(M - nM);
+#pragma unroll
+      for (int j = 0; j < V; ++j) o[j] *= f;
+      den *= f;
+      M = nM;
+    }
+    const float w = lse == -INFINITY ? 0.f : exp2f(lse - M);
+    den += warp_sum(w);
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      if (k < cnt) {
+        const float wk = __shfl_sync(FULL, w, k);
+#pragma unroll
+        for (int j = 0; j < V; ++j) o[j] = fmaf(wk, v[k][j], o[j]);
       }
     }
   }
 }
 
-// Calls seg(b, t0, t1, L, slot) for every sequence piece of this CTA, on the partition that merge_kernel
-// recomputes (decode_common.cuh): fixed splits of the keys that the window leaves, or runs of the
-// concatenated pages.
-template <int THREADS, typename SegFn>
-__device__ __forceinline__ void kv_pieces(const SplitArgs &a, unsigned *flags, SegFn &&seg) {
-  if (a.num_splits > 0) {
-    const int b = blockIdx.x / a.num_splits, s = blockIdx.x % a.num_splits;
-    const SeqSpan sp = seq_span(a, b, threadIdx.x == 0 && s == 0 && blockIdx.y == 0 ? flags : nullptr);
-    const int span = (sp.L - sp.lo + a.num_splits - 1) / a.num_splits;
-    const long long t0 = sp.lo + static_cast<long long>(s) * span;
-    const int t1 = static_cast<int>(min(t0 + span, static_cast<long long>(sp.L)));
-    if (t0 < t1) seg(b, static_cast<int>(t0), t1, sp.L, static_cast<long long>(blockIdx.x));
-    return;
+// The finished row (b, hq): the sink joins the denominator, then o / den, and the log-sum-exp on request. A row without
+// keys is zero (lse: the sink alone, or -inf); a NaN among the scores makes row and lse NaN.
+template <int D>
+__device__ __forceinline__ void kv_finish(const SplitArgs &a, int b, int hq, int lane, float sink2, float M, float den,
+                                          float (&o)[D / 32]) {
+  constexpr int V = D / 32;
+  if (sink2 > -INFINITY) {
+    const float nM = fmaxf(M, sink2);
+    const float f = M == -INFINITY ? 0.f : exp2f(M - nM);
+#pragma unroll
+    for (int j = 0; j < V; ++j) o[j] *= f;
+    den = den * f + exp2f(sink2 - nM);
+    M = nM;
   }
-  __shared__ long long s_scan[THREADS / 32];
-  __shared__ long long s_first_p;
-  __shared__ int s_first_b;
+  const float inv = den != 0.f ? 1.f / den : 0.f;
+#pragma unroll
+  for (int j = 0; j < V; ++j) o[j] *= inv;
+  const long long row = static_cast<long long>(b) * a.Hq + hq;
+  if (a.lse_out != nullptr && lane == 0) a.lse_out[row] = den != 0.f ? (M + log2f(den)) * 0.6931471805599453f : -INFINITY;
+  store_out<D>(a, row, lane, o);
+}
+__device__ __forceinline__ float kv_sink2(const SplitArgs &a, int hq) {
+  return a.sinks != nullptr ? __ldg(a.sinks + hq) * 1.4426950408889634f : -INFINITY;
+}
+
+// Inclusive sum over the first 256 threads (all threads of the block call it); the total to *total.
+__device__ __forceinline__ long long kv_scan(long long v, long long *scratch, long long *total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  auto scan = [&](long long v, long long *total) -> long long {  // inclusive, over the block
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long n = __shfl_up_sync(FULL, v, o);
-      if (lane >= o) v += n;
-    }
-    if (lane == 31) s_scan[warp] = v;
-    __syncthreads();
-    long long before = 0, all = 0;
-#pragma unroll
-    for (int w = 0; w < THREADS / 32; ++w) {
-      const long long x = s_scan[w];
-      if (w < warp) before += x;
-      all += x;
-    }
-    __syncthreads();
-    *total = all;
-    return v + before;
-  };
-  const bool report = blockIdx.x == 0 && blockIdx.y == 0;
-  const long long C = gridDim.x, c = blockIdx.x;
-  long long pages = 0;
-  long long keep_np = 0, keep_incl = 0;  // this thread's sequence, when one round covers the batch
-  for (int base = 0; base < a.B; base += THREADS) {
-    const int b = base + threadIdx.x;
-    const long long np = b < a.B ? seq_span(a, b, report ? flags : nullptr).np : 0;
-    long long chunk;
-    const long long incl = scan(np, &chunk);
-    keep_np = np;
-    keep_incl = incl;
-    pages += chunk;
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long n = __shfl_up_sync(FULL, v, o);
+    if (lane >= o) v += n;
   }
-  const long long q = pages / C, r = pages % C;
-  const long long pb = c * q + min(c, r), pe = pb + q + (c < r ? 1 : 0);
-  if (pb >= pe) return;
-  if (threadIdx.x == 0) s_first_b = -1;
+  if (lane == 31 && warp < 8) scratch[warp] = v;
   __syncthreads();
-  long long running = 0;
-  for (int base = 0; base < a.B; base += THREADS) {
-    const int b = base + threadIdx.x;
-    long long np = keep_np, incl = keep_incl;
-    if (a.B > THREADS) {
-      np = b < a.B ? seq_span(a, b, nullptr).np : 0;
-      long long chunk;
-      incl = scan(np, &chunk) + running;
-      running += chunk;
-    }
-    const long long excl = incl - np;
-    if (np > 0 && excl <= pb && pb < incl) {
-      s_first_b = b;
-      s_first_p = excl;
-    }
-    __syncthreads();
-    if (s_first_b >= 0) break;  // uniform: written before the barrier, at most once
-    __syncthreads();
+  long long before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) {
+    const long long x = scratch[w];
+    if (w < warp) before += x;
+    all += x;
   }
-  int b = s_first_b;
-  long long P = s_first_p;
-  while (P < pe && b >= 0 && b < a.B) {
-    const SeqSpan sp = seq_span(a, b, nullptr);
-    if (sp.np > 0) {
-      const long long lo = max(pb, P) - P, hi = min(pe, P + sp.np) - P;
-      const int t0 = max(static_cast<int>((sp.f + lo) * kPage), sp.lo);
-      const int t1 = static_cast<int>(min((sp.f + hi) * kPage, static_cast<long long>(sp.L)));
-      if (threadIdx.x == 0 && blockIdx.y == 0) {
-        if (P >= pb) a.seg_first[b] = static_cast<int>(c);
-        if (P + sp.np <= pe) a.seg_last[b] = static_cast<int>(c);
-      }
-      seg(b, t0, t1, sp.L, c + b);
-    }
-    P += sp.np;
-    ++b;
-  }
+  __syncthreads();
+  *total = all;
+  return v + before;
 }
-
-constexpr int kKvWarps = 4;
-constexpr int kKvMaxResident = 3;  // CTAs of an SM, by registers: 3 at up to 168, else 2
-template <int D, int CT, int NT>
-constexpr int kv_resident() { return NT == 1 && D < 256 && CT != KV_E4M3 ? 3 : 2; }
+extern __shared__ __align__(1024) uint8_t kvq_kv_dsmem[];
 
 template <int D, int CT, int NT, bool FOLD, bool MODS>
-__global__ void __launch_bounds__(32 * kKvWarps, kv_resident<D, CT, NT>()) decode_kv_kernel(const __grid_constant__ KvParams p) {
+__global__ void __launch_bounds__(kKvThreads, 1) decode_kv_kernel(const __grid_constant__ KvParams p) {
+  using Gm = KvGeom<D, CT>;
+  __shared__ __align__(8) uint64_t s_full[kKvMaxSlots], s_empty[kKvMaxSlots];
+  __shared__ uint8_t s_bad[kKvMaxSlots];  // pages of a slot without a block of their own, a bit each
+  __shared__ volatile int s_failed;
+  __shared__ long long s_scan[8], s_first_p;
+  __shared__ int s_first_b;
   asm volatile("griddepcontrol.launch_dependents;");  // let the merge kernel's launch begin early
-  const int warp = threadIdx.x >> 5;
-  const int hv = blockIdx.y * p.s.heads_per_cta + warp % p.s.heads_per_cta;  // (kv head, block of query heads)
-  const int h = hv / p.col_blocks, cb = hv % p.col_blocks, sub = warp / p.s.heads_per_cta;
-  kv_pieces<32 * kKvWarps>(p.s, &g_flags_decode_kv, [&](int b, int t0, int t1, int L, long long slot) {
-    kv_piece<D, CT, NT, FOLD, MODS>(p, b, h, cb, sub, t0, t1, L, slot);
-  });
+  const SplitArgs &a = p.s;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int W = a.warps_per_head, HB = a.heads_per_cta, CB = p.col_blocks;
+  if (tid < p.slots) {
+    mbar_init(smem_u32(&s_full[tid]), 1);
+    mbar_init(smem_u32(&s_empty[tid]), W * HB * CB);
+    mbar_init_fence();
+  }
+  if (tid == 0) {
+    s_first_b = a.B;
+    s_failed = 0;
+  }
+  __syncthreads();
+
+  // ---- where the CTA's run starts
+  const bool report = blockIdx.x == 0 && blockIdx.y == 0;  // each clamped length once
+  KvCursor cur = {};
+  if (a.num_splits > 0) {
+    cur.b = blockIdx.x / a.num_splits;
+    if (report)
+      for (int b = tid; b < a.B; b += kKvThreads) clamped_len(a, b, &g_flags_decode_kv);
+  } else {
+    long long pages = 0, chunk = 0, np = 0, incl = 0;
+    for (int base = 0; base < a.B; base += 256) {
+      const int b = base + tid;
+      np = tid < 256 && b < a.B ? seq_span(a, b, report ? &g_flags_decode_kv : nullptr).np : 0;
+      incl = kv_scan(np, s_scan, &chunk);
+      pages += chunk;
+    }
+    const long long q = pages / gridDim.x, r = pages % gridDim.x, x = blockIdx.x;
+    cur.pb = x * q + min(x, r);  // the first r runs are a page longer
+    cur.pe = cur.pb + q + (x < r ? 1 : 0);
+    long long before = 0;
+    for (int base = 0; base < a.B; base += 256) {
+      const int b = base + tid;
+      if (a.B > 256) {
+        np = tid < 256 && b < a.B ? seq_span(a, b, nullptr).np : 0;
+        incl = kv_scan(np, s_scan, &chunk) + before;
+        before += chunk;
+      }
+      if (np > 0 && incl - np <= cur.pb && cur.pb < incl) {
+        s_first_b = b;
+        s_first_p = incl - np;
+      }
+    }
+    __syncthreads();
+    cur.b = s_first_b;
+    cur.P = s_first_p;
+  }
+  // ring slots start at the first 1024-byte aligned offset of the dynamic buffer (the swizzle's unit); a slot is
+  // [page][head][K or V of 16 tokens]
+  const uint32_t dbase = smem_u32(kvq_kv_dsmem), off = (1024u - (dbase & 1023u)) & 1023u;
+  KvRing rg;
+  rg.stride = W * HB * Gm::HALF;
+  rg.n = p.slots;
+  rg.full = smem_u32(&s_full[0]);
+  rg.empty = smem_u32(&s_empty[0]);
+  rg.at = rg.phase = 0;
+  const int h0 = blockIdx.y / p.col_groups * HB, cg = blockIdx.y % p.col_groups;
+  KvPiece pc;
+
+  if (warp == kKvWarps) {  // ---- producer: lane j < W brings page j of each slot
+    const int tpb = p.bs / kPage;  // tiles of a block
+    const bool withhold = p.withhold >= 0 && report;
+    rg.addr = dbase + off + lane * HB * Gm::HALF;
+    rg.phase = 1;  // the slots start empty
+    uint32_t issued = 0;
+    bool more = next_piece(a, cur, pc);
+    while (more) {
+      const int32_t *bt = p.block_table + static_cast<long long>(pc.b) * p.bt_stride;
+      auto load_id = [&](int i) { return lane < W && i + lane < pc.n ? __ldg(bt + (pc.page + i + lane) / tpb) : 0; };
+      int id[4] = {load_id(0), load_id(W), load_id(2 * W), load_id(3 * W)};  // the next slots' blocks, ahead of their use
+      for (int i = 0; i < pc.n && more; i += W) {
+        const bool mine = lane < W && i + lane < pc.n, ok = id[0] >= 0 && id[0] < p.num_blocks;
+        if (mine && !ok) atomicOr(&g_flags_decode_kv, ERR_BLOCK);
+        const int blk = ok ? id[0] : 0, row = (pc.page + i + lane) % tpb * kPage;
+        const unsigned bad = __ballot_sync(FULL, mine && !ok);
+        id[0] = id[1];
+        id[1] = id[2];
+        id[2] = id[3];
+        id[3] = load_id(i + 4 * W);
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          const uint32_t empty = rg.empty + 8 * rg.at, full = rg.full + 8 * rg.at;
+          if (!__all_sync(FULL, mbar_test_wait(empty, rg.phase))) {  // until the workers release the slot, or one gave up
+            const uint64_t start = global_ns();
+            while (!__all_sync(FULL, mbar_try_wait_sleep(empty, rg.phase, 20000u))) {
+              if (__any_sync(FULL, s_failed || global_ns() - start > p.wait_ns)) {
+                more = false;
+                break;
+              }
+            }
+            if (!more) break;
+          }
+          if (!(withhold && rg.at == static_cast<uint32_t>(p.withhold))) {
+            if (lane == 0) {
+              if (v == 0) s_bad[rg.at] = static_cast<uint8_t>(bad);
+              mbar_arrive_expect_tx(full, min(W, pc.n - i) * HB * Gm::HALF);
+            }
+            __syncwarp();
+            if (mine) tma_load_5d(rg.addr + rg.at * rg.stride, v == 0 ? &p.k : &p.v, 0, row, 0, h0, blk, full);
+          }
+          ++issued;
+          rg.advance();
+        }
+      }
+      if (more) more = next_piece(a, cur, pc);
+    }
+    // the copies land before the CTA can exit, whatever became of the workers (bounded: one may be withheld)
+    const uint32_t n = issued < rg.n ? issued : rg.n;
+    for (uint32_t e = issued - n; e < issued; ++e) mbar_wait(rg.full + 8 * (e % rg.n), (e / rg.n) & 1, 100000000ull);
+    return;
+  }
+
+  // ---- worker: page sub of each slot, kv head h, block cb of its query heads
+  const int sub = warp / (HB * CB), hl = warp / CB % HB, cb = cg * CB + warp % CB;
+  if (sub < W) {
+    const uint32_t mine = off + (sub * HB + hl) * Gm::HALF;
+    rg.addr = dbase + mine;
+    bool ok = true;
+    while (ok && next_piece(a, cur, pc)) {
+      ok = kv_piece<D, CT, NT, FOLD, MODS>(p, rg, kvq_kv_dsmem + mine, s_bad, h0 + hl, cb, sub, pc);
+      if (a.num_splits == 0 && tid == 0 && blockIdx.y == 0) {  // the sequence's first and last CTA, for the merge
+        const SeqSpan sp = seq_span(a, pc.b, nullptr);
+        if (pc.page == sp.f) a.seg_first[pc.b] = static_cast<int>(blockIdx.x);
+        if (pc.page + pc.n == sp.f + sp.np) a.seg_last[pc.b] = static_cast<int>(blockIdx.x);
+      }
+    }
+    if (!ok && lane == 0) s_failed = 1;
+  }
+  if (p.direct) {  // the partials of this CTA's sequence, joined here
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+    const int b = blockIdx.x;
+    const long long lo = static_cast<long long>(b) * W, hi = seq_span(a, b, nullptr).np > 0 ? lo + W : lo;
+    const int cols = CB * 8 * NT;
+    for (int i = warp; i < HB * cols; i += kKvWarps) {
+      const int col = cg * cols + i % cols, hq = (h0 + i / cols) * a.G + col;
+      if (col >= a.G) continue;
+      float M, den, o[D / 32];
+      kv_join<D>(a, hq, lo, hi, 1, lane, M, den, o);
+      kv_finish<D>(a, b, hq, lane, kv_sink2(a, hq), M, den, o);
+    }
+  }
+}
+
+// WPR warps for each output row (b, hq). Launched as a programmatic dependent of the split kernel: lengths and slot
+// ranges (recomputed for B <= 256, else from seg_first / seg_last) come before griddepcontrol.wait.
+template <int D, int WPR>
+__global__ void __launch_bounds__(256) kv_merge_kernel(const SplitArgs a) {
+  constexpr int V = D / 32;
+  __shared__ long long s_scan[8], s_page[256];
+  __shared__ float s_o[8][WPR > 1 ? D : 1], s_m[8], s_d[8];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const long long idx = static_cast<long long>(blockIdx.x) * (8 / WPR) + warp / WPR;
+  const bool live = idx < static_cast<long long>(a.B) * a.Hq;
+  const int b = live ? static_cast<int>(idx / a.Hq) : 0, hq = live ? static_cast<int>(idx % a.Hq) : 0;
+  const SeqSpan sp = live ? seq_span(a, b, nullptr) : SeqSpan{0, 0, 0, 0};
+  const float sink2 = kv_sink2(a, hq);
+  long long lo = 0, hi = 0;
+  const bool scan = a.num_splits == 0 && a.B <= 256;  // uniform
+  if (scan) {
+    const long long np = tid < a.B ? seq_span(a, tid, nullptr).np : 0;
+    long long pages;
+    s_page[tid] = kv_scan(np, s_scan, &pages) - np;
+    __syncthreads();
+    if (sp.np > 0) {
+      const long long q = pages / a.seg_ctas, r = pages % a.seg_ctas;
+      lo = run_of_page(s_page[b], q, r) + b;
+      hi = run_of_page(s_page[b] + sp.np - 1, q, r) + b + 1;
+    }
+  } else if (a.num_splits > 0 && sp.np > 0) {
+    const int per = (sp.np + a.num_splits - 1) / a.num_splits;
+    lo = static_cast<long long>(b) * a.num_splits;
+    hi = lo + (sp.np + per - 1) / per;
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!scan && a.num_splits == 0 && sp.np > 0) {
+    lo = static_cast<long long>(__ldcg(a.seg_first + b)) + b;
+    hi = static_cast<long long>(__ldcg(a.seg_last + b)) + b + 1;
+  }
+  lo = max(0LL, min(lo, a.slots)) * a.warps_per_head;  // never index outside the workspace
+  hi = max(lo, min(hi, a.slots) * a.warps_per_head);
+  float M, den, o[V];
+  kv_join<D>(a, hq, lo + warp % WPR, hi, WPR, lane, M, den, o);
+  if constexpr (WPR > 1) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) s_o[warp][lane * V + j] = o[j];
+    if (lane == 0) {
+      s_m[warp] = M;
+      s_d[warp] = den;
+    }
+    __syncthreads();
+    if (warp % WPR != 0) return;
+    float top = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < WPR; ++k) top = fmaxf(top, s_m[warp + k]);
+    M = top;
+    den = 0.f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) o[j] = 0.f;
+#pragma unroll
+    for (int k = 0; k < WPR; ++k) {
+      const float m = s_m[warp + k], f = m == -INFINITY ? (s_d[warp + k] == 0.f ? 0.f : 1.f) : exp2f(m - top);
+      den += s_d[warp + k] * f;
+#pragma unroll
+      for (int j = 0; j < V; ++j) o[j] = fmaf(s_o[warp + k][lane * V + j], f, o[j]);
+    }
+  }
+  if (live) kv_finish<D>(a, b, hq, lane, sink2, M, den, o);
 }
 
 bool take_flags_decode_kv(cudaStream_t stream, unsigned *host_word) {
@@ -575,63 +809,102 @@ bool take_flags_decode_kv(cudaStream_t stream, unsigned *host_word) {
 // accumulators of 16 would not fit the registers).
 static int kv_tiles(int G, int D) { return G <= 8 || D == 256 ? 1 : 2; }
 
-static bool kv_plan(int B, int Hq, int Hk, int D, int num_splits, SplitPlan *plan) {
-  const int G = Hq / Hk, cols = 8 * kv_tiles(G, D);
-  const long long units = static_cast<long long>(Hk) * ((G + cols - 1) / cols);
-  int hpc = kKvWarps;
-  while (units % hpc) hpc /= 2;
-  plan->heads_per_cta = hpc;
-  plan->head_groups = static_cast<int>(units / hpc);
-  plan->warps_per_head = kKvWarps / hpc;
-  if (units / hpc > 65535) return false;
+// CTAs along the sequences so that all head groups' CTAs run at once: one more would run alone, behind the rest
+// (5 head groups, D = 256: 63 us with 155 CTAs on 152 SMs, 49 us with 150).
+static int kv_wave(int ctas, int head_groups) { return head_groups < ctas ? ctas / head_groups : 1; }
+
+// A call's geometry: HB kv heads x CB blocks of query heads x W pages are a CTA's workers; head_groups: grid.y.
+struct KvPlan {
+  int HB, CB, W, col_groups, head_groups, grid_x;
+  long long slots;  // of W partials for each query head
+};
+static bool kv_plan(int B, int Hq, int Hk, int D, int num_splits, KvPlan *plan) {
+  const int G = Hq / Hk, cols = 8 * kv_tiles(G, D), blocks = (G + cols - 1) / cols;
+  plan->col_groups = (blocks + kKvWarps - 1) / kKvWarps;
+  plan->CB = (blocks + plan->col_groups - 1) / plan->col_groups;
+  int hb = kKvWarps;
+  while (hb * plan->CB > kKvWarps || Hk % hb) hb /= 2;
+  plan->HB = hb;
+  plan->W = kKvWarps / (hb * plan->CB);
+  const long long groups = static_cast<long long>(Hk / hb) * plan->col_groups;
+  if (groups > 65535) return false;
+  plan->head_groups = static_cast<int>(groups);
   if (num_splits > 0) {
     const long long ctas = static_cast<long long>(B) * num_splits;
     if (ctas > 0x7fffffffLL) return false;
-    plan->seg_ctas = static_cast<int>(ctas);
+    plan->grid_x = static_cast<int>(ctas);
     plan->slots = ctas;
   } else {
     const int sms = sm_count();
     if (sms <= 0) return false;
-    plan->seg_ctas = (kKvMaxResident * sms + plan->head_groups - 1) / plan->head_groups;
-    plan->slots = static_cast<long long>(plan->seg_ctas) + B;
+    plan->grid_x = kv_wave(sms, plan->head_groups);
+    plan->slots = static_cast<long long>(plan->grid_x) + B;
   }
   return true;
 }
+static size_t kv_workspace(int B, int Hq, int D, const KvPlan &plan) {
+  const size_t rows = static_cast<size_t>(plan.slots) * plan.W * Hq;
+  return round256(rows * D * sizeof(float)) + round256(rows * sizeof(float)) + 2 * round256(static_cast<size_t>(B) * sizeof(int32_t));
+}
 
-template <int D, int CT, int NT, bool FOLD>
-static kvq_status launch_kv(KvParams &p, const SplitPlan &plan, bool mods, cudaStream_t s) {
-  if (p.s.num_splits == 0)  // one wave: the workspace has room for kKvMaxResident CTAs of an SM
-    p.s.seg_ctas = (kv_resident<D, CT, NT>() * sm_count() + plan.head_groups - 1) / plan.head_groups;
-  const dim3 grid(p.s.seg_ctas, plan.head_groups);
-  if (mods)
-    decode_kv_kernel<D, CT, NT, FOLD, true><<<grid, 32 * kKvWarps, 0, s>>>(p);
-  else
-    decode_kv_kernel<D, CT, NT, FOLD, false><<<grid, 32 * kKvWarps, 0, s>>>(p);
-  if (cudaGetLastError() != cudaSuccess) return KVQ_ERR_CUDA;
-  const long long rows = static_cast<long long>(p.s.B) * p.s.Hq;
-  if (launch_dependent(merge_kernel<D, true>, dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256), s, p.s) != cudaSuccess)
+template <int D, int CT, int NT, bool FOLD, bool MODS>
+static kvq_status launch_kv(KvParams &p, int head_groups, const kvq_paged_kv *cache, cudaStream_t s) {
+  using Gm = KvGeom<D, CT>;
+  const int64_t es = CT == KV_E4M3 ? 1 : 2;
+  const int HB = p.s.heads_per_cta;
+  if (!paged_tensor_map(cache->k, Gm::ROW, Gm::PB, HB, cache->k_stride_token * es, cache->k_stride_head * es,
+                        cache->k_stride_block * es, p.bs, p.s.Hk, cache->num_blocks, &p.k) ||
+      !paged_tensor_map(cache->v, Gm::ROW, Gm::PB, HB, cache->v_stride_token * es, cache->v_stride_head * es,
+                        cache->v_stride_block * es, p.bs, p.s.Hk, cache->num_blocks, &p.v))
     return KVQ_ERR_CUDA;
+  const int slot = p.s.warps_per_head * HB * Gm::HALF, fit = Gm::RING / slot;
+  p.slots = fit < kKvMaxSlots ? fit : kKvMaxSlots;
+  const size_t smem = static_cast<size_t>(p.slots) * slot + 1024;
+  static size_t attr_done[kMaxDevices] = {};
+  if (ensure_dynamic_smem(decode_kv_kernel<D, CT, NT, FOLD, MODS>, Gm::RING + 1024, attr_done) != cudaSuccess) return KVQ_ERR_CUDA;
+  decode_kv_kernel<D, CT, NT, FOLD, MODS><<<dim3(p.s.seg_ctas, head_groups), kKvThreads, smem, s>>>(p);
   return launch_status();
 }
 
-template <int D, int CT>
-static kvq_status launch_kv_tiles(KvParams &p, const SplitPlan &plan, bool mods, cudaStream_t s) {
+template <int D, int CT, bool MODS>
+static kvq_status launch_kv_tiles(KvParams &p, int groups, const kvq_paged_kv *cache, cudaStream_t s) {
   if constexpr (D < 256) {
-    if (kv_tiles(p.s.G, D) == 2) return launch_kv<D, CT, 2, false>(p, plan, mods, s);
+    if (kv_tiles(p.s.G, D) == 2) return launch_kv<D, CT, 2, false, MODS>(p, groups, cache, s);
   }
-  if constexpr (CT == KV_BF16) {
-    if (p.s.G <= 4) return launch_kv<D, CT, 1, true>(p, plan, mods, s);
+  return p.s.G <= 4 ? launch_kv<D, CT, 1, true, MODS>(p, groups, cache, s) : launch_kv<D, CT, 1, false, MODS>(p, groups, cache, s);
+}
+
+template <int D, bool MODS>
+static kvq_status launch_kv_type(KvParams &p, int groups, const kvq_paged_kv *cache, cudaStream_t s) {
+  switch (cache->dtype) {
+    case KVQ_BF16: return launch_kv_tiles<D, KV_BF16, MODS>(p, groups, cache, s);
+    case KVQ_F16: return launch_kv_tiles<D, KV_F16, MODS>(p, groups, cache, s);
+    default: return launch_kv_tiles<D, KV_E4M3, MODS>(p, groups, cache, s);
   }
-  return launch_kv<D, CT, 1, false>(p, plan, mods, s);
 }
 
 template <int D>
-static kvq_status launch_kv_type(KvParams &p, const SplitPlan &plan, kvq_dtype dtype, bool mods, cudaStream_t s) {
-  switch (dtype) {
-    case KVQ_BF16: return launch_kv_tiles<D, KV_BF16>(p, plan, mods, s);
-    case KVQ_F16: return launch_kv_tiles<D, KV_F16>(p, plan, mods, s);
-    default: return launch_kv_tiles<D, KV_E4M3>(p, plan, mods, s);
+static kvq_status launch_kv_merge(const KvParams &p, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const long long rows = static_cast<long long>(p.s.B) * p.s.Hq;
+  // partials of a row, on average: one warp reads 16 of them a round trip
+  const long long parts = static_cast<long long>(p.s.num_splits > 0 ? p.s.num_splits : p.s.seg_ctas / p.s.B + 1) * p.s.warps_per_head;
+  cudaError_t e;
+  if (parts > 16) {
+    cfg.gridDim = dim3(static_cast<unsigned>(rows));
+    e = cudaLaunchKernelEx(&cfg, kv_merge_kernel<D, 8>, p.s);
+  } else {
+    cfg.gridDim = dim3(static_cast<unsigned>((rows + 7) / 8));
+    e = cudaLaunchKernelEx(&cfg, kv_merge_kernel<D, 1>, p.s);
   }
+  return e == cudaSuccess ? launch_status() : KVQ_ERR_CUDA;
 }
 
 }  // namespace kvq
@@ -640,9 +913,9 @@ using namespace kvq;
 
 extern "C" size_t kvq_decode_kv_workspace_bytes(int32_t B, int32_t Hq, int32_t Hk, int32_t D, int32_t num_splits) {
   if (B < 0 || Hq < 1 || Hk < 1 || Hq % Hk || num_splits < 0 || (D != 64 && D != 128 && D != 256)) return 0;
-  SplitPlan plan;
+  KvPlan plan;
   if (!kv_plan(B, Hq, Hk, D, num_splits, &plan)) return 0;
-  return workspace_bytes(B, Hq, D, plan);
+  return kv_workspace(B, Hq, D, plan);
 }
 
 extern "C" kvq_status kvq_decode_kv(const void *q, kvq_dtype q_dtype, const kvq_paged_kv *cache,
@@ -666,14 +939,15 @@ extern "C" kvq_status kvq_decode_kv(const void *q, kvq_dtype q_dtype, const kvq_
   if (cache->block_size % kPage) return KVQ_ERR_UNSUPPORTED;
   if (!(softmax_scale > 0.f) || !(softmax_scale < INFINITY)) return KVQ_ERR_INVALID_ARG;
   if (static_cast<long long>(max_blocks) * cache->block_size > 0x7fffffffLL - kPage) return KVQ_ERR_UNSUPPORTED;
-  SplitPlan plan;
+  KvPlan plan;
   if (!kv_plan(B, Hq, Hk, D, num_splits, &plan)) return KVQ_ERR_UNSUPPORTED;
   if (B == 0) return KVQ_OK;
   if (!q || !block_table || !seq_lens || !out || !workspace || max_blocks < 1) return KVQ_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(out, 16) ||
       !aligned(workspace, 16))
     return KVQ_ERR_INVALID_ARG;
-  if (workspace_bytes < kvq::workspace_bytes(B, Hq, D, plan)) return KVQ_ERR_WORKSPACE;
+  if (workspace_bytes < kv_workspace(B, Hq, D, plan)) return KVQ_ERR_WORKSPACE;
+  if (B > 0x7fffffff / Hq) return KVQ_ERR_UNSUPPORTED;
 
   KvParams p = {};
   SplitArgs &sa = p.s;
@@ -685,35 +959,36 @@ extern "C" kvq_status kvq_decode_kv(const void *q, kvq_dtype q_dtype, const kvq_
   sa.Hk = Hk;
   sa.G = Hq / Hk;
   sa.Q = 1;
-  sa.heads_per_cta = plan.heads_per_cta;
-  sa.warps_per_head = plan.warps_per_head;
-  sa.seg_ctas = plan.seg_ctas;
+  sa.heads_per_cta = plan.HB;
+  sa.warps_per_head = plan.W;
   sa.slots = plan.slots;
-  workspace_carve(workspace, B, Hq, D, plan, &sa.part_o, &sa.part_lse, &sa.seg_first, &sa.seg_last);
+  // One CTA for each sequence and head group, one launch: asked for by num_splits = 1, or where the tables allow at most
+  // kDirectPages pages for each worker.
+  p.direct = num_splits == 1 ||
+             (num_splits == 0 && B <= plan.grid_x && sa.max_blocks <= static_cast<long long>(kDirectPages) * plan.W);
+  if (p.direct) sa.num_splits = 1;
+  sa.seg_ctas = p.direct ? B : plan.grid_x;
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  const size_t part_rows = static_cast<size_t>(plan.slots) * plan.W * Hq;
+  sa.part_o = reinterpret_cast<float *>(ws);
+  sa.part_lse = reinterpret_cast<float *>(ws += round256(part_rows * D * sizeof(float)));
+  sa.seg_first = reinterpret_cast<int32_t *>(ws += round256(part_rows * sizeof(float)));
+  sa.seg_last = reinterpret_cast<int32_t *>(ws + round256(static_cast<size_t>(B) * sizeof(int32_t)));
   sa.out = out;
   sa.out_dtype = out_dtype;
   sa.window = mods ? mods->sliding_window : 0;
   sa.sinks = mods ? mods->sinks : nullptr;
   sa.lse_out = mods ? mods->lse_out : nullptr;
-  const long long es = cache->dtype == KVQ_E4M3 ? 1 : 2;
   p.q = q;
   p.q_f16 = q_dtype == KVQ_F16;
-  p.k = static_cast<const uint8_t *>(cache->k);
-  p.v = static_cast<const uint8_t *>(cache->v);
-  p.k_block = cache->k_stride_block * es;
-  p.k_token = cache->k_stride_token * es;
-  p.k_head = cache->k_stride_head * es;
-  p.v_block = cache->v_stride_block * es;
-  p.v_token = cache->v_stride_token * es;
-  p.v_head = cache->v_stride_head * es;
   p.k_scale = cache->k_scale;
   p.v_scale = cache->v_scale;
   p.block_table = block_table;
   p.bt_stride = max_blocks;
   p.bs = cache->block_size;
   p.num_blocks = cache->num_blocks;
-  const int cols = 8 * kv_tiles(sa.G, D);
-  p.col_blocks = (sa.G + cols - 1) / cols;
+  p.col_blocks = plan.CB;
+  p.col_groups = plan.col_groups;
   p.sc_log2 = static_cast<float>(static_cast<double>(softmax_scale) * 1.4426950408889634);
   const double cap2 = mods ? static_cast<double>(mods->softcap) * 1.4426950408889634 : 0.0;
   p.cap2 = static_cast<float>(cap2);
@@ -721,7 +996,16 @@ extern "C" kvq_status kvq_decode_kv(const void *q, kvq_dtype q_dtype, const kvq_
   p.alibi = mods ? mods->alibi_slopes : nullptr;
   const bool scored = p.cap2 > 0.f || p.alibi != nullptr;  // the window and the sinks need no kernel of their own
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (D == 64) return launch_kv_type<64>(p, plan, cache->dtype, scored, s);
-  if (D == 128) return launch_kv_type<128>(p, plan, cache->dtype, scored, s);
-  return launch_kv_type<256>(p, plan, cache->dtype, scored, s);
+  p.wait_ns = debug_wait_ns();
+  p.withhold = debug_take_withhold();  // one call only
+  const int groups = plan.head_groups;
+  kvq_status st;
+  if (D == 64)
+    st = scored ? launch_kv_type<64, true>(p, groups, cache, s) : launch_kv_type<64, false>(p, groups, cache, s);
+  else if (D == 128)
+    st = scored ? launch_kv_type<128, true>(p, groups, cache, s) : launch_kv_type<128, false>(p, groups, cache, s);
+  else
+    st = scored ? launch_kv_type<256, true>(p, groups, cache, s) : launch_kv_type<256, false>(p, groups, cache, s);
+  if (st != KVQ_OK || p.direct) return st;
+  return D == 64 ? launch_kv_merge<64>(p, s) : D == 128 ? launch_kv_merge<128>(p, s) : launch_kv_merge<256>(p, s);
 }

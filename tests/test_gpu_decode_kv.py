@@ -293,3 +293,17 @@ def test_binding_checks():
                     (dict(workspace=torch.empty(64, dtype=torch.uint8, device="cuda")), kvq.KvqError)):
         with pytest.raises(err):
             call(**kw)
+
+
+@pytest.mark.parametrize("cache,D", [(BF, 128), (E4, 64), (F16, 256)])
+@pytest.mark.parametrize("stage", [0, 1, 2])
+def test_bounded_wait_is_flagged_and_the_next_call_is_exact(cache, D, stage):
+    """A copy that never comes (withheld on the host's order, nothing faults): flag 8, and the context goes on."""
+    c = Case([700, 33, 100], 8, 2, D, cache, seed=15)
+    kvq.kvq_debug_set_wait(5_000_000, stage)
+    try:
+        c.run(num_splits=1)  # the first CTA has all of sequence 0: its first warp goes round its ring
+        assert kvq.kvq_device_error() == (kvq.KVQ_ERR_OUT_OF_RANGE, 8)
+    finally:
+        kvq.kvq_debug_set_wait(0, -1)
+    c.check()
