@@ -5,15 +5,23 @@
 // turn, so positions[t] * f_i mod 2^64 is the angle modulo a turn, exactly; its top 32 bits, signed,
 // times 2^-31 are the angle in units of pi in [-1, 1), which sincospif takes as it is: no range
 // reduction, and the same accuracy (2^-25 turns) at any position. cos and sin belong to the token,
-// not to the head: a CTA computes them once into shared memory, and all heads of q and k use them.
+// not to the head: they go to shared memory once, and all heads of q and k use them.
 //
-// What bounds it: HBM. Every element is read once and written once. A thread moves 16-byte chunks:
-// the two chunks of eight elements whose pairs belong together (half layout), or one (interleaved
-// pairs, elements that pass, values). Products and sums are fp32 and rounded once, to the output's or
-// the cache's type.
+// What bounds it: HBM. Every element is read once and written once. A thread moves 16-byte chunks in twos: the two
+// chunks of eight elements whose pairs belong together (half layout), or two chunks a half row apart (interleaved
+// pairs, elements that pass, values). Products and sums are fp32 and rounded once, to the output's or the cache's type.
 //
-// Heads whose pairs do not keep to such chunks (rotary_dim / 2 not a multiple of 8, odd strides) take
+// A warp takes one token, or one of `parts` shares of its rows where tokens are few; every share computes the angles
+// again, so warps need nothing from each other. A lane keeps its place in the row (32 lanes are 32 / 2^n rows of 2^n
+// pairs of chunks), so its eight cos / sin stay in registers and a step is two loads, the arithmetic, two stores and
+// four additions. Before that (places walked lane by lane, angles read from shared memory for each item, a division
+// here and there) the prefill of 16384 tokens was bound by its instructions: 71-76 us, now 65, against a floor of 59.
+// Loading the first rows of q, k and v ahead of the position and the slot costs registers and with them warps: 69 us.
+//
+// Heads whose pairs do not keep to such chunks (rotary_dim / 2 not a multiple of 8, odd strides, D > 512) take
 // the element path: a thread owns a pair (or one element that passes), so that q_out == q stays safe.
+
+#include <type_traits>
 
 #include "kvq_device.cuh"
 #include "kvq_host.h"
@@ -42,7 +50,11 @@ struct WriteKvParams {
   int32_t interleaved;
   float factor;
   int32_t T, D;
+  int32_t bs_shift;            // log2 of the block size, or -1
+  int32_t row_shift;           // chunk path: log2 of the lanes that a row takes
 };
+
+constexpr int kWriteWarps = 4;  // of a CTA: small ones, so that the last wave is full
 
 enum : int { kFp8Dst = 3 };  // destination type of the pools beside KVQ_BF16 / KVQ_F16 / KVQ_F32
 
@@ -52,30 +64,43 @@ __device__ __forceinline__ float load1(const void *p, long long i) {
   else if constexpr (T == KVQ_F16) return __half2float(static_cast<const __half *>(p)[i]);
   else return static_cast<const float *>(p)[i];
 }
-__device__ __forceinline__ uint8_t to_fp8(float x, float scale) {
-  const float y = __fdiv_rn(x, scale);  // the conversion itself saturates at 448 and keeps a NaN
-  return static_cast<uint8_t>(__nv_cvt_float_to_fp8(y, __NV_SATFINITE, __NV_E4M3));
+// FP8 codes of x times inv, the reciprocal of the head's scale: the conversion saturates at 448 and keeps a NaN
+__device__ __forceinline__ uint8_t to_fp8(float x, float inv) {
+  return static_cast<uint8_t>(__nv_cvt_float_to_fp8(x * inv, __NV_SATFINITE, __NV_E4M3));
+}
+__device__ __forceinline__ float fp8_inv(const float *scales, int head) {
+  return scales != nullptr ? __frcp_rn(__ldg(scales + head)) : 1.f;
 }
 template <int T>
-__device__ __forceinline__ void store1(void *p, long long i, float x, float scale) {
+__device__ __forceinline__ void store1(void *p, long long i, float x, float inv) {
   if constexpr (T == KVQ_BF16) static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(x);
   else if constexpr (T == KVQ_F16) static_cast<__half *>(p)[i] = __float2half_rn(x);
   else if constexpr (T == KVQ_F32) static_cast<float *>(p)[i] = x;
-  else static_cast<uint8_t *>(p)[i] = to_fp8(x, scale);
+  else static_cast<uint8_t *>(p)[i] = to_fp8(x, inv);
 }
 
+// eight elements as they lie in memory
 template <int T>
-__device__ __forceinline__ void load8(const void *p, long long i, float (&x)[8]) {
-  if constexpr (T == KVQ_F32) {
-    const float4 *s = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
-    const float4 a = s[0], b = s[1];
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-  } else {
-    const uint4 r = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + i);
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+struct Raw8 {
+  uint32_t w[T == KVQ_F32 ? 8 : 4];
+  __device__ __forceinline__ void load(const void *p, long long i) {
+    const uint4 *s = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(p) + i * (T == KVQ_F32 ? 4 : 2));
+#pragma unroll
+    for (int k = 0; k < (T == KVQ_F32 ? 2 : 1); ++k) {
+      const uint4 r = s[k];
+      w[4 * k] = r.x;
+      w[4 * k + 1] = r.y;
+      w[4 * k + 2] = r.z;
+      w[4 * k + 3] = r.w;
+    }
+  }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      if constexpr (T == KVQ_BF16) {
+      if constexpr (T == KVQ_F32) {
+        x[2 * j] = __uint_as_float(w[2 * j]);
+        x[2 * j + 1] = __uint_as_float(w[2 * j + 1]);
+      } else if constexpr (T == KVQ_BF16) {
         x[2 * j] = __uint_as_float(w[j] << 16);
         x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
       } else {
@@ -85,9 +110,9 @@ __device__ __forceinline__ void load8(const void *p, long long i, float (&x)[8])
       }
     }
   }
-}
+};
 template <int T>
-__device__ __forceinline__ void store8(void *p, long long i, const float (&x)[8], float scale) {
+__device__ __forceinline__ void store8(void *p, long long i, const float (&x)[8], float inv) {
   if constexpr (T == KVQ_F32) {
     float4 *d = reinterpret_cast<float4 *>(static_cast<float *>(p) + i);
     d[0] = make_float4(x[0], x[1], x[2], x[3]);
@@ -98,7 +123,8 @@ __device__ __forceinline__ void store8(void *p, long long i, const float (&x)[8]
     for (int j = 0; j < 2; ++j) {
       w[j] = 0;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) w[j] |= static_cast<uint32_t>(to_fp8(x[4 * j + e], scale)) << (8 * e);
+      for (int e = 0; e < 4; e += 2)
+        w[j] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(x[4 * j + e] * inv, x[4 * j + e + 1] * inv), __NV_SATFINITE, __NV_E4M3)) << (8 * e);
     }
     *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p) + i) = make_uint2(w[0], w[1]);
   } else {
@@ -116,132 +142,162 @@ __device__ __forceinline__ void store8(void *p, long long i, const float (&x)[8]
   }
 }
 
-// cos and sin of the token's pairs, times the factor, into shared memory
-__device__ __forceinline__ void fill_angles(const WriteKvParams &p, int pos, float2 *cs) {
-  for (int i = threadIdx.x; i < p.half; i += blockDim.x) {
+// cos and sin of the token's pairs, times the factor, into the warp's shared memory
+__device__ __forceinline__ void fill_angles(const WriteKvParams &p, int pos, int lane, float2 *cs) {
+  for (int i = lane; i < p.half; i += 32) {
     const uint64_t turn = static_cast<uint64_t>(static_cast<uint32_t>(pos)) * __ldg(p.freqs + i);  // mod 2^64: mod a turn
     const float x = static_cast<float>(static_cast<int32_t>(turn >> 32)) * 4.656612873077393e-10f;  // 2^-31: units of pi
     float s, c;
     sincospif(x, &s, &c);
     cs[i] = make_float2(c * p.factor, s * p.factor);
   }
+  __syncwarp();
+}
+
+// A lane's place in a row: chunk a, and b where there is one (b < 0: none).
+struct Place {
+  int a, b;
+  bool live, turns;
+};
+// cos and sin of the lane's pairs: (a_e, b_e) of the half layout, or pairs 0 .. 3 of chunk a and 4 .. 7 of chunk b
+struct Angles {
+  float2 f[8];
+};
+
+// Rows r0, r0 + dr, ... < heads of one row set, two at a time: src and dst are the token's (t, 0, 0) elements.
+template <int IN, int OUT>
+__device__ __forceinline__ void write_rows(const void *src, long long src_h, void *dst, long long dst_h, int heads, int r0,
+                                           int dr, const Place &pl, bool interleaved, const Angles &an, const float *scales) {
+  auto turn = [&](float (&x)[8], float (&y)[8]) {
+    if (!pl.turns) return;
+    if (interleaved) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 f = an.f[e], g = an.f[e + 4];
+        const float u = x[2 * e], v = x[2 * e + 1], c = y[2 * e], d = y[2 * e + 1];
+        x[2 * e] = u * f.x - v * f.y;
+        x[2 * e + 1] = v * f.x + u * f.y;
+        y[2 * e] = c * g.x - d * g.y;
+        y[2 * e + 1] = d * g.x + c * g.y;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float2 f = an.f[e];
+        const float u = x[e], v = y[e];
+        x[e] = u * f.x - v * f.y;
+        y[e] = v * f.x + u * f.y;
+      }
+    }
+  };
+  auto finish = [&](const Raw8<IN> &ra, const Raw8<IN> &rb, int row) {
+    float x[8], y[8], inv = 1.f;
+    ra.get(x);
+    rb.get(y);
+    turn(x, y);
+    if constexpr (OUT == kFp8Dst) inv = fp8_inv(scales, row);
+    const long long at = row * dst_h;
+    store8<OUT>(dst, at + 8 * pl.a, x, inv);
+    if (pl.b >= 0) store8<OUT>(dst, at + 8 * pl.b, y, inv);
+  };
+  if (!pl.live) return;
+  for (int r = r0; r < heads; r += 2 * dr) {
+    Raw8<IN> xa, xb = {}, ya = {}, yb = {};
+    const bool two = r + dr < heads;
+    const long long at = r * src_h, next = (r + dr) * src_h;
+    xa.load(src, at + 8 * pl.a);
+    if (pl.b >= 0) xb.load(src, at + 8 * pl.b);
+    if (two) {
+      ya.load(src, next + 8 * pl.a);
+      if (pl.b >= 0) yb.load(src, next + 8 * pl.b);
+    }
+    finish(xa, xb, r);
+    if (two) finish(ya, yb, r + dr);
+  }
 }
 
 // IN: type of q, k, v and q_out / k_out. POOL: type of the pools (IN, or FP8), or -1: k_out, no cache.
 template <int IN, int POOL, bool VEC>
-__global__ void __launch_bounds__(256) write_kv_kernel(const WriteKvParams p) {
+__global__ void __launch_bounds__(32 * kWriteWarps) write_kv_kernel(const WriteKvParams p) {
   extern __shared__ __align__(16) float2 kvq_angles[];
-  const int t = blockIdx.x;
-  const int pos = p.positions != nullptr ? __ldg(p.positions + t) : 0;
-  if (pos < 0) return;  // padding
-  long long slot = -1;
-  if constexpr (POOL >= 0) {
-    slot = __ldg(p.slots + t);
-    if (slot >= p.num_blocks * p.bs) {
-      if (threadIdx.x == 0) atomicOr(&g_flags_write_kv, ERR_SLOT);
-      slot = -1;
-    }
-  }
+  constexpr int KOUT = POOL >= 0 ? POOL : IN;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int t = blockIdx.x * kWriteWarps + warp, part = blockIdx.y;
+  if (t >= p.T) return;
   const bool rot = p.positions != nullptr;
-  if (rot) {
-    fill_angles(p, pos, kvq_angles);
-    __syncthreads();
-  }
-  long long kd = 0, vd = 0;  // element offsets of the token in the pools
-  if (POOL >= 0 && slot >= 0) {
-    const long long blk = slot / p.bs, row = slot - blk * p.bs;
-    kd = blk * p.k_block + row * p.k_token;
-    vd = blk * p.v_block + row * p.v_token;
-  }
-  const bool kv = POOL < 0 || slot >= 0;
+  constexpr int EI = IN == KVQ_F32 ? 4 : 2, EK = POOL == kFp8Dst ? 1 : EI;
+  const uint8_t *q_src = static_cast<const uint8_t *>(p.q.src) + t * p.q.src_t * EI;
+  const uint8_t *k_src = static_cast<const uint8_t *>(p.k.src) + t * p.k.src_t * EI;
+  [[maybe_unused]] const uint8_t *v_src = static_cast<const uint8_t *>(p.v.src) + t * p.v.src_t * EI;
   const int half = rot ? p.half : 0, R = 2 * half;
-  // items: a row's pairs (VEC: chunks of 8 pairs, or of 4 interleaved) and the elements that pass
-  const int pass = VEC ? (p.D - R) / 8 : p.D - R;
-  const int pairs = VEC ? (p.interleaved ? R / 8 : half / 8) : half;
-  const int per = pairs + pass, rows = p.q.heads + (kv ? p.k.heads : 0);
-  const int vper = VEC ? p.D / 8 : p.D, items = rows * per + (kv && POOL >= 0 ? p.v.heads * vper : 0);
-  for (int i = threadIdx.x; i < items; i += blockDim.x) {
-    int row, j, which;
-    if (i < rows * per) {
-      row = i / per;
-      j = i - row * per;
-      which = row < p.q.heads ? 0 : 1;
-      if (which) row -= p.q.heads;
-    } else {
-      row = (i - rows * per) / vper;
-      j = (i - rows * per) - row * vper + pairs;  // past the pairs: passes
-      which = 2;
+  // places: pairs of chunks of the rotated part (rc chunks), then of the rest (pc)
+  const int lanes = 1 << p.row_shift, j = lane & (lanes - 1);
+  const int r0 = (lane >> p.row_shift) + part * (32 >> p.row_shift), dr = (32 >> p.row_shift) * gridDim.y;
+  const int rc = R / 8, pc = (p.D - R) / 8, ri = (rc + 1) / 2, pi = (pc + 1) / 2, vc = p.D / 8, vi = (vc + 1) / 2;
+  Place pl;
+  pl.turns = j < ri;
+  pl.live = j < ri + pi;
+  pl.a = pl.turns ? j : rc + j - ri;
+  pl.b = pl.turns ? (j + ri < rc ? j + ri : -1) : (j - ri + pi < pc ? rc + j - ri + pi : -1);
+  const Place pv = {j, j + vi < vc ? j + vi : -1, j < vi, false};
+  const int pos = rot ? __ldg(p.positions + t) : 0;
+  if (pos < 0) return;  // padding
+  bool kv = true;
+  long long kd = 0, vd = 0;  // element offsets of the token in the pools
+  if constexpr (POOL >= 0) {
+    const long long slot = __ldg(p.slots + t);
+    kv = slot >= 0 && slot < p.num_blocks * p.bs;
+    if (slot >= 0 && !kv && part == 0 && lane == 0) atomicOr(&g_flags_write_kv, ERR_SLOT);
+    if (kv) {
+      const long long blk = p.bs_shift >= 0 ? slot >> p.bs_shift : slot / p.bs, row = slot - blk * p.bs;
+      kd = blk * p.k_block + row * p.k_token;
+      vd = blk * p.v_block + row * p.v_token;
     }
-    const RowSet &rs = which == 0 ? p.q : which == 1 ? p.k : p.v;
-    const long long so = t * rs.src_t + row * rs.src_h;
-    const bool pool = POOL >= 0 && which != 0;
-    const long long dd = (pool ? (which == 1 ? kd : vd) : t * rs.dst_t) + row * rs.dst_h;
-    float scale = 1.f;
-    if constexpr (POOL == kFp8Dst) {
-      const float *sc = which == 1 ? p.k_scale : p.v_scale;
-      if (pool && sc != nullptr) scale = __ldg(sc + row);
-    }
-    const int d0 = which == 2 ? 0 : R;  // first element that passes
-    if constexpr (VEC) {
-      auto put = [&](long long d, const float (&x)[8]) {
-        if constexpr (POOL >= 0) {
-          if (pool) {
-            store8<POOL>(rs.dst, dd + d, x, scale);
-            return;
-          }
-        }
-        store8<IN>(rs.dst, dd + d, x, scale);
-      };
-      float x[8];
-      if (j >= pairs) {
-        const int d = d0 + 8 * (j - pairs);
-        load8<IN>(rs.src, so + d, x);
-        put(d, x);
-      } else if (p.interleaved) {
-        load8<IN>(rs.src, so + 8 * j, x);
+  } else {
+    kd = t * p.k.dst_t;
+  }
+  uint8_t *q_dst = static_cast<uint8_t *>(p.q.dst) + t * p.q.dst_t * EI, *k_dst = static_cast<uint8_t *>(p.k.dst) + kd * EK;
+  [[maybe_unused]] uint8_t *v_dst = static_cast<uint8_t *>(p.v.dst) + vd * EK;
+  float2 *cs = kvq_angles + static_cast<size_t>(warp) * p.half;
+  if (rot) fill_angles(p, pos, lane, cs);
+
+  if constexpr (VEC) {
+    Angles an = {};
+    if (pl.turns) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 cs = kvq_angles[4 * j + e];
-          const float a = x[2 * e], b = x[2 * e + 1];
-          x[2 * e] = a * cs.x - b * cs.y;
-          x[2 * e + 1] = b * cs.x + a * cs.y;
-        }
-        put(8 * j, x);
-      } else {
-        float y[8];
-        load8<IN>(rs.src, so + 8 * j, x);
-        load8<IN>(rs.src, so + half + 8 * j, y);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float2 cs = kvq_angles[8 * j + e];
-          const float a = x[e], b = y[e];
-          x[e] = a * cs.x - b * cs.y;
-          y[e] = b * cs.x + a * cs.y;
-        }
-        put(8 * j, x);
-        put(half + 8 * j, y);
-      }
-    } else {
-      auto put = [&](long long d, float x) {
-        if constexpr (POOL >= 0) {
-          if (pool) {
-            store1<POOL>(rs.dst, dd + d, x, scale);
-            return;
-          }
-        }
-        store1<IN>(rs.dst, dd + d, x, scale);
-      };
-      if (j >= pairs) {
-        const int d = d0 + j - pairs;
-        put(d, load1<IN>(rs.src, so + d));
-      } else {
-        const int da = p.interleaved ? 2 * j : j, db = p.interleaved ? 2 * j + 1 : j + half;
-        const float2 cs = kvq_angles[j];
-        const float a = load1<IN>(rs.src, so + da), b = load1<IN>(rs.src, so + db);
-        put(da, a * cs.x - b * cs.y);
-        put(db, b * cs.x + a * cs.y);
-      }
+      for (int e = 0; e < 8; ++e)
+        an.f[e] = !p.interleaved ? cs[8 * pl.a + e] : e < 4 ? cs[4 * pl.a + e] : pl.b >= 0 ? cs[4 * pl.b + e - 4] : make_float2(0.f, 0.f);
     }
+    write_rows<IN, IN>(q_src, p.q.src_h, q_dst, p.q.dst_h, p.q.heads, r0, dr, pl, p.interleaved, an, nullptr);
+    if (!kv) return;
+    write_rows<IN, KOUT>(k_src, p.k.src_h, k_dst, p.k.dst_h, p.k.heads, r0, dr, pl, p.interleaved, an, p.k_scale);
+    if constexpr (POOL >= 0)
+      write_rows<IN, POOL>(v_src, p.v.src_h, v_dst, p.v.dst_h, p.v.heads, r0, dr, pv, false, an, p.v_scale);
+  } else {
+    const int first = 32 * part + lane, step = 32 * gridDim.y;
+    auto rows = [&](auto out, const void *src, long long src_h, void *dst, long long dst_h, int heads, int pairs, const float *scales) {
+      constexpr int OUT = decltype(out)::value;
+      const int per = p.D - pairs;  // a pair, or an element that passes
+      for (int i = first; i < heads * per; i += step) {
+        const int row = i / per, j = i - row * per;
+        const long long so = row * src_h, at = row * dst_h;
+        const float inv = OUT == kFp8Dst ? fp8_inv(scales, row) : 1.f;
+        if (j >= pairs) {
+          store1<OUT>(dst, at + j + pairs, load1<IN>(src, so + j + pairs), inv);
+        } else {
+          const int da = p.interleaved ? 2 * j : j, db = p.interleaved ? 2 * j + 1 : j + half;
+          const float2 f = cs[j];
+          const float a = load1<IN>(src, so + da), b = load1<IN>(src, so + db);
+          store1<OUT>(dst, at + da, a * f.x - b * f.y, inv);
+          store1<OUT>(dst, at + db, b * f.x + a * f.y, inv);
+        }
+      }
+    };
+    rows(std::integral_constant<int, IN>{}, q_src, p.q.src_h, q_dst, p.q.dst_h, p.q.heads, half, nullptr);
+    if (!kv) return;
+    rows(std::integral_constant<int, KOUT>{}, k_src, p.k.src_h, k_dst, p.k.dst_h, p.k.heads, half, p.k_scale);
+    if constexpr (POOL >= 0)
+      rows(std::integral_constant<int, POOL>{}, v_src, p.v.src_h, v_dst, p.v.dst_h, p.v.heads, 0, p.v_scale);
   }
 }
 
@@ -259,17 +315,31 @@ static bool chunked(const RowSet &r) {
   return r.heads == 0 || (aligned(r.src, 16) && aligned(r.dst, 16) && r.src_t % 8 == 0 && r.src_h % 8 == 0 &&
                           r.dst_t % 8 == 0 && r.dst_h % 8 == 0);
 }
+// Pairs of chunks of a row: of its rotated part and of the rest.
+static int row_places(const WriteKvParams &p) {
+  const int rc = p.half / 4, pc = p.D / 8 - rc;
+  return (rc + 1) / 2 + (pc + 1) / 2;
+}
 static bool chunked_pairs(const WriteKvParams &p) {
-  return p.D % 8 == 0 && (p.positions == nullptr || (p.interleaved ? p.half % 4 == 0 : p.half % 8 == 0));
+  return p.D % 8 == 0 && row_places(p) <= 32 && (p.positions == nullptr || (p.interleaved ? p.half % 4 == 0 : p.half % 8 == 0));
 }
 
 template <int IN, int POOL>
-static kvq_status launch_write_kv(const WriteKvParams &p, bool vec, cudaStream_t s) {
-  const size_t smem = p.positions != nullptr ? static_cast<size_t>(p.half) * sizeof(float2) : 0;
+static kvq_status launch_write_kv(WriteKvParams &p, bool vec, cudaStream_t s) {
+  // shares of a token: 16 warps an SM, at most as many as have a row (elements: 32 of them)
+  const int rows = p.q.heads > p.k.heads ? p.q.heads : p.k.heads;
+  p.row_shift = 0;
+  while ((1 << p.row_shift) < row_places(p)) ++p.row_shift;
+  const long long per_warp = vec ? 32 >> p.row_shift : 1;
+  const long long most = vec ? (rows + per_warp - 1) / per_warp : (static_cast<long long>(rows) * p.D + 31) / 32;
+  const long long want = (16LL * (sm_count() > 0 ? sm_count() : 1) + p.T - 1) / p.T;
+  const long long parts = want < most ? want : most;
+  const size_t smem = p.positions != nullptr ? static_cast<size_t>(kWriteWarps) * p.half * sizeof(float2) : 0;
+  const dim3 grid((p.T + kWriteWarps - 1) / kWriteWarps, static_cast<unsigned>(parts < 65535 ? parts : 65535));
   if (vec)
-    write_kv_kernel<IN, POOL, true><<<p.T, 256, smem, s>>>(p);
+    write_kv_kernel<IN, POOL, true><<<grid, 32 * kWriteWarps, smem, s>>>(p);
   else
-    write_kv_kernel<IN, POOL, false><<<p.T, 256, smem, s>>>(p);
+    write_kv_kernel<IN, POOL, false><<<grid, 32 * kWriteWarps, smem, s>>>(p);
   return launch_status();
 }
 
@@ -406,6 +476,9 @@ extern "C" kvq_status kvq_write_kv(const void *key, int64_t k_stride_t, int64_t 
   p.k_scale = cache->k_scale;
   p.v_scale = cache->v_scale;
   p.bs = cache->block_size;
+  p.bs_shift = -1;
+  for (int i = 0; i < 31; ++i)
+    if (p.bs == 1 << i) p.bs_shift = i;
   p.num_blocks = cache->num_blocks;
   p.T = T;
   p.D = D;

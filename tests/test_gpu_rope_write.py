@@ -48,7 +48,7 @@ def positions_of(T, seed, pad=0, high=40000):
 @pytest.mark.parametrize("dtype", [BF, F16, F32])
 @pytest.mark.parametrize("interleaved", [False, True])
 @pytest.mark.parametrize("D,R", [(128, 128), (128, 64), (64, 64), (80, 80), (80, 40), (256, 32), (64, 2), (24, 20), (7, 6),
-                                 (1024, 1024)])
+                                 (1024, 1024), (512, 512), (512, 72), (104, 24)])
 def test_rope(D, R, interleaved, dtype):
     T, Hq, Hk, pad = 13, 5, 2, 3
     x = torch.randn((T, (Hq + Hk) * D), generator=torch.Generator().manual_seed(D + R)).to(dtype).cuda()
