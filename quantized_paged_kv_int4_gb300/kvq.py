@@ -2,13 +2,14 @@
 
 Every function takes CUDA torch tensors, checks dtype / device / layout, and passes raw device
 pointers plus the current torch stream to the C ABI; all compute runs in libkvq's kernels.
-There is no fallback: if libkvq.so cannot be built or loaded, or a call returns an error status,
-an exception is raised.
+There is no fallback: if libkvq.so (or kvq_native.so, the binding of the serving-step calls) cannot be
+built or loaded, or a call returns an error status, an exception is raised.
 """
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
-import struct
 import threading
 
 import torch
@@ -513,114 +514,25 @@ def kvq_device_error(stream=None):
 # A serving step over 16-bit and FP8 paged caches: block tables and slot maps, rotary positions, the
 # cache write and the split decode.
 # ----------------------------------------------------------------------------------------------
-# These calls are small and frequent (a step of 32 tokens), so their checks are written to be quick: one
-# expression for each tensor, the structs packed as bytes, the raw handle of the current stream.
-_CACHE_CODES = {torch.bfloat16: KVQ_BF16, torch.float16: KVQ_F16, torch.float8_e4m3fn: KVQ_E4M3}
-_Tensor, _I32, _I64, _F32, _E4M3 = torch.Tensor, torch.int32, torch.int64, torch.float32, torch.float8_e4m3fn
-_pack_paged_kv = struct.Struct("@PPqqqqqqPPiiq").pack  # kvq_paged_kv
-_pack_rotary = struct.Struct("@PPiif0P").pack            # kvq_rotary
-_pack_mods = struct.Struct("@ifPPiPPi0P").pack           # kvq_score_mods
-_NO_ROWS = (None, 0, 0, None, 0, 0, 0)
+# These calls are small and frequent (a step of 32 tokens), so their arguments are checked and passed by a native module
+# (native/binding.cpp) instead of ctypes: about 1 us a call instead of 6 to 10.
+_native_module = None
 
 
-def _device_of(t, name):
-    """The index of a CUDA tensor's device."""
-    if not isinstance(t, _Tensor) or not t.is_cuda:
-        raise TypeError("%s must be a CUDA tensor" % name)
-    return t.get_device()
-
-
-def _on(t, name, dtype, dev):
-    """t: a contiguous tensor of dtype on device dev; its data pointer."""
-    if not (isinstance(t, _Tensor) and t.dtype is dtype and t.get_device() == dev and t.is_contiguous()):
-        _need(t, name, dtype)
-        raise ValueError("%s is on %s, the call on cuda:%d" % (name, t.device, dev))
-    return t.data_ptr()
-
-
-def _on_or_none(t, name, dtype, dev, size):
-    if t is None:
-        return None
-    p = _on(t, name, dtype, dev)
-    if t.numel() != size:
-        raise ValueError("%s must have %d entries, got %d" % (name, size, t.numel()))
-    return p
-
-
-def _call(name, dev, stream, *args):
-    """kvq_<name>(*args, stream) with device dev current and, by default, that device's current stream."""
-    fn = getattr(lib(), name)
-    s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-    if torch._C._cuda_getDevice() == dev:
-        status = fn(*args, s)
-    else:
-        with torch.cuda.device(dev):
-            status = fn(*args, s)
-    if status != KVQ_OK:
-        raise KvqError(status, name)
-
-
-def _rows(t, name, dtype, dev, T, D):
-    """(pointer, token stride, head stride, heads) of a tensor [T, heads, D] with a contiguous last dim."""
-    if not isinstance(t, _Tensor) or not t.is_cuda:
-        raise TypeError("%s must be a CUDA tensor" % name)
-    if t.dtype is not dtype:
-        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if t.dim() != 3 or t.shape[0] != T or t.shape[2] != D:
-        raise ValueError("%s must be [%d, heads, %d], got %s" % (name, T, D, tuple(t.shape)))
-    st, sh, sd = t.stride()
-    if sd != 1 and D > 1:
-        raise ValueError("%s must have a contiguous last dim" % name)
-    if t.get_device() != dev:
-        raise ValueError("%s is on %s, the call on cuda:%d" % (name, t.device, dev))
-    return t.data_ptr(), st, sh, t.shape[1]
-
-
-def _rows_out(x, out, name, dtype, dev, T, D):
-    """(out, arguments) of a rotated row set: x's pointer and strides, out's, the heads; out is new when None."""
-    p, st, sh, heads = _rows(x, name, dtype, dev, T, D)
-    if out is None:
-        out = torch.empty((T, heads, D), dtype=dtype, device=x.device)
-    po, ot, oh, oheads = _rows(out, name + "_out", dtype, dev, T, D)
-    if oheads != heads:
-        raise ValueError("%s_out must have %s's shape" % (name, name))
-    return out, (p, st, sh, po, ot, oh, heads)
-
-
-def _rotary(positions, freqs, interleaved, attn_factor, T, D, dev):
-    pos = _on(positions, "positions", _I32, dev)
-    fr = _on(freqs, "freqs", _I64, dev)
-    half = freqs.numel()
-    if positions.numel() != T:
-        raise ValueError("positions must have T = %d entries" % T)
-    if freqs.dim() != 1 or not 1 <= half <= D // 2:
-        raise ValueError("freqs must be [rotary_dim / 2] with rotary_dim <= D = %d" % D)
-    return _pack_rotary(pos, fr, 2 * half, 1 if interleaved else 0, attn_factor)
-
-
-def _paged_kv(k_cache, v_cache, k_scale, v_scale, dtype, dev, Hk, D):
-    """(kvq_paged_kv, Hk) of two [num_blocks, block_size, Hk, D] views with any strides but the last; Hk None: any.
-    dtype: the type of the rows beside the cache."""
-    if not isinstance(k_cache, _Tensor) or not isinstance(v_cache, _Tensor) or not k_cache.is_cuda or not v_cache.is_cuda:
-        raise TypeError("k_cache / v_cache must be CUDA tensors")
-    code = _CACHE_CODES.get(k_cache.dtype)
-    if code is None or v_cache.dtype is not k_cache.dtype:
-        raise TypeError("k_cache / v_cache must both be bfloat16, float16 or float8_e4m3fn")
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
-        raise ValueError("k_cache / v_cache must both be [num_blocks, block_size, Hk, D]")
-    nb, bs, heads, d = k_cache.shape
-    ks, vs = k_cache.stride(), v_cache.stride()
-    if ks[3] != 1 or vs[3] != 1:
-        raise ValueError("k_cache / v_cache must have a contiguous last dim")
-    if d != D or (Hk is not None and heads != Hk):
-        raise ValueError("the cache's heads are [%d, %d], the call's [%s, %d]" % (heads, d, heads if Hk is None else Hk, D))
-    if code != KVQ_E4M3 and (k_cache.dtype is not dtype or k_scale is not None or v_scale is not None):
-        raise TypeError("a 16-bit cache has the type of the rows (%s) and no scales" % dtype)
-    if k_cache.get_device() != dev or v_cache.get_device() != dev:
-        raise ValueError("the caches are on %s and %s, the call on cuda:%d" % (k_cache.device, v_cache.device, dev))
-    return _pack_paged_kv(k_cache.data_ptr(), v_cache.data_ptr(), ks[0], ks[1], ks[2], vs[0], vs[1], vs[2],
-                          _on_or_none(k_scale, "k_scale", _F32, dev, heads) or 0,
-                          _on_or_none(v_scale, "v_scale", _F32, dev, heads) or 0, code, bs, nb), heads
+def _native():
+    """The loaded kvq_native (built in-tree with libkvq when missing or stale)."""
+    global _native_module
+    if _native_module is None:
+        lib()
+        with _lock:
+            if _native_module is None:
+                loader = importlib.machinery.ExtensionFileLoader("kvq_native", _build.build_native())
+                spec = importlib.util.spec_from_file_location("kvq_native", loader.path, loader=loader)
+                m = importlib.util.module_from_spec(spec)
+                loader.exec_module(m)
+                m.set_error(KvqError)
+                _native_module = m
+    return _native_module
 
 
 def kvq_plan_step(context_lens, query_lens, block_table, free_blocks, cursor, block_size, num_blocks, rows=None,
@@ -634,43 +546,9 @@ def kvq_plan_step(context_lens, query_lens, block_table, free_blocks, cursor, bl
     requests' rows. Outputs that are not given are allocated (batch_table only when given; T rows of
     positions and slot_mapping: required then unless one of them is given).
     Returns (seq_lens, query_start_loc, positions, slot_mapping)."""
-    dev = _device_of(context_lens, "context_lens")
-    B = context_lens.numel()
-    p_context = _on(context_lens, "context_lens", _I32, dev)
-    p_table = _on(block_table, "block_table", _I32, dev)
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [rows, max_blocks]")
-    n_rows, width = block_table.shape
-    if (free_blocks is None) != (cursor is None):
-        raise ValueError("free_blocks and cursor go together")
-    p_free = None if free_blocks is None else _on(free_blocks, "free_blocks", _I32, dev)
-    if T is None:
-        given = positions if positions is not None else slot_mapping
-        if given is None:
-            raise ValueError("T, the rows of positions and slot_mapping, is needed")
-        T = given.numel()
-    if seq_lens is None:
-        seq_lens = torch.empty(B, dtype=_I32, device=context_lens.device)
-    if query_start_loc is None:
-        query_start_loc = torch.empty(B + 1, dtype=_I32, device=context_lens.device)
-    if positions is None:
-        positions = torch.empty(T, dtype=_I32, device=context_lens.device)
-    if slot_mapping is None:
-        slot_mapping = torch.empty(T, dtype=_I64, device=context_lens.device)
-    p_batch = None
-    if batch_table is not None:
-        p_batch = _on(batch_table, "batch_table", _I32, dev)
-        if batch_table.shape != (B, width):
-            raise ValueError("batch_table must be [B, max_blocks] = %s" % ((B, width),))
-    p_cursor = _on_or_none(cursor, "cursor", _I64, dev, 1)
-    _call("kvq_plan_step", dev, stream, p_context, _on_or_none(query_lens, "query_lens", _I32, dev, B),
-          _on_or_none(rows, "rows", _I32, dev, B), p_table, width, n_rows, p_free,
-          0 if free_blocks is None else free_blocks.numel(), p_cursor,
-          p_cursor if cursor_out is None else _on_or_none(cursor_out, "cursor_out", _I64, dev, 1),
-          _on_or_none(seq_lens, "seq_lens", _I32, dev, B), _on_or_none(query_start_loc, "query_start_loc", _I32, dev, B + 1),
-          _on_or_none(positions, "positions", _I32, dev, T), _on_or_none(slot_mapping, "slot_mapping", _I64, dev, T),
-          p_batch, B, T, block_size, num_blocks)
-    return seq_lens, query_start_loc, positions, slot_mapping
+    return (_native_module or _native()).plan_step(
+        context_lens, query_lens, block_table, free_blocks, cursor, block_size, num_blocks, rows, batch_table, cursor_out,
+        seq_lens, query_start_loc, positions, slot_mapping, T, stream)
 
 
 def kvq_rope_frequencies(rotary_dim, base=10000.0, scaling="none", factor=1.0, original=0.0, low=0.0, high=0.0,
@@ -691,24 +569,7 @@ def kvq_rope(q, k, positions, freqs, interleaved=False, attn_factor=1.0, q_out=N
     """Rotary positions: q [T, Hq, D] and k [T, Hk, D] (bf16 / f16 / f32, last dim contiguous; either may be None) ->
     (q_out, k_out), new contiguous tensors by default; pass q_out=q, k_out=k for in place. Rows whose position is
     negative are padding and stay unwritten."""
-    ref = q if q is not None else k
-    dev = _device_of(ref, "q")
-    code = _OUT_CODES.get(ref.dtype)
-    if code is None:
-        raise TypeError("q / k must be bfloat16, float16 or float32, got %s" % ref.dtype)
-    if ref.dim() != 3:
-        raise ValueError("q / k must be [T, heads, D]")
-    T, _, D = ref.shape
-    if (q is None and q_out is not None) or (k is None and k_out is not None):
-        raise ValueError("an output without its input")
-    q_args = k_args = _NO_ROWS
-    if q is not None:
-        q_out, q_args = _rows_out(q, q_out, "q", ref.dtype, dev, T, D)
-    if k is not None:
-        k_out, k_args = _rows_out(k, k_out, "k", ref.dtype, dev, T, D)
-    _call("kvq_rope", dev, stream, *q_args, *k_args, _rotary(positions, freqs, interleaved, attn_factor, T, D, dev), code,
-          T, D)
-    return q_out, k_out
+    return (_native_module or _native()).rope(q, k, positions, freqs, interleaved, attn_factor, q_out, k_out, stream)
 
 
 def kvq_write_kv(key, value, k_cache, v_cache, slot_mapping, k_scale=None, v_scale=None, q=None, positions=None,
@@ -717,32 +578,8 @@ def kvq_write_kv(key, value, k_cache, v_cache, slot_mapping, k_scale=None, v_sca
     [num_blocks, block_size, Hk, D] views of the same type or float8_e4m3fn (codes of x / scale[head]).
     With positions (int32 [T]) and freqs (kvq_rope_frequencies) the keys are rotated on the way, and q
     [T, Hq, D] into q_out. Returns q_out (None without q)."""
-    dev, dtype = _device_of(key, "key"), key.dtype
-    if dtype is not torch.bfloat16 and dtype is not torch.float16:
-        raise TypeError("key must be a CUDA bfloat16 or float16 tensor")
-    if key.dim() != 3:
-        raise ValueError("key must be [T, Hk, D]")
-    T, Hk, D = key.shape
-    pk, kt, kh, _ = _rows(key, "key", dtype, dev, T, D)
-    pv, vt, vh, heads = _rows(value, "value", dtype, dev, T, D)
-    if heads != Hk:
-        raise ValueError("value must have key's shape")
-    kv, _ = _paged_kv(k_cache, v_cache, k_scale, v_scale, dtype, dev, Hk, D)
-    slots = _on_or_none(slot_mapping, "slot_mapping", _I64, dev, T)
-    if slots is None:
-        raise TypeError("slot_mapping must be a CUDA tensor")
-    if (positions is None) != (freqs is None):
-        raise ValueError("positions and freqs go together")
-    rot = None if positions is None else _rotary(positions, freqs, interleaved, attn_factor, T, D, dev)
-    q_args = _NO_ROWS
-    if q is not None:
-        if rot is None:
-            raise ValueError("q is only rotated: positions and freqs are needed")
-        q_out, q_args = _rows_out(q, q_out, "q", dtype, dev, T, D)
-    elif q_out is not None:
-        raise ValueError("q_out without q")
-    _call("kvq_write_kv", dev, stream, pk, kt, kh, pv, vt, vh, kv, slots, *q_args, rot, _OUT_CODES[dtype], T, Hk, D)
-    return q_out
+    return (_native_module or _native()).write_kv(key, value, k_cache, v_cache, slot_mapping, k_scale, v_scale, q, positions,
+                                                  freqs, interleaved, attn_factor, q_out, stream)
 
 
 def kvq_decode_kv_workspace_bytes(B, Hq, Hk, D, num_splits=0):
@@ -755,44 +592,9 @@ def kvq_decode_kv(q, k_cache, v_cache, block_table, seq_lens, softmax_scale, k_s
     """Decode attention of one token per sequence over a 16-bit or FP8 paged cache: q [B, Hq, D] (bf16 / f16),
     k_cache / v_cache as kvq_write_kv -> out [B, Hq, D] (q's type by default). Modifiers and lse_out (fp32
     [B, Hq]) as kvq_decode_int4. Returns out."""
-    dev, dtype = _device_of(q, "q"), q.dtype
-    if dtype is not torch.bfloat16 and dtype is not torch.float16:
-        raise TypeError("q must be a CUDA bfloat16 or float16 tensor")
-    if q.dim() != 3:
-        raise ValueError("q must be [B, Hq, D]")
-    B, Hq, D = q.shape
-    pq = _on(q, "q", dtype, dev)
-    kv, Hk = _paged_kv(k_cache, v_cache, k_scale, v_scale, dtype, dev, None, D)
-    p_table = _on(block_table, "block_table", _I32, dev)
-    if block_table.dim() != 2 or block_table.shape[0] != B:
-        raise ValueError("block_table must be [B, max_blocks] with B = %d" % B)
-    p_lens = _on(seq_lens, "seq_lens", _I32, dev)
-    if seq_lens.numel() != B:
-        raise ValueError("seq_lens must have B = %d entries" % B)
-    if out is None:
-        out = torch.empty((B, Hq, D), dtype=out_dtype or dtype, device=q.device)
-    _need(out, "out")
-    out_code = _out_code(out.dtype)
-    p_out = _on(out, "out", out.dtype, dev)
-    if out.shape != q.shape:
-        raise ValueError("out must have q's shape %s, got %s" % (tuple(q.shape), tuple(out.shape)))
-    mods = None
-    if sliding_window or softcap or sinks is not None or alibi_slopes is not None or lse_out is not None:
-        p_lse = 0
-        if lse_out is not None:
-            p_lse = _on(lse_out, "lse_out", _F32, dev)
-            if lse_out.shape != (B, Hq):
-                raise ValueError("lse_out must be [%d, %d]" % (B, Hq))
-        mods = _pack_mods(sliding_window, softcap, _on_or_none(sinks, "sinks", _F32, dev, Hq) or 0,
-                          _on_or_none(alibi_slopes, "alibi_slopes", _F32, dev, Hq) or 0, 1, p_lse, 0, 0)
-    if workspace is None:
-        need = lib().kvq_decode_kv_workspace_bytes(B, Hq, Hk, D, num_splits) if Hk else 0
-        workspace = torch.empty((max(need, 16),), dtype=torch.uint8, device=q.device)
-        if stream is not None:  # freed here, in use there until the call's kernels end
-            workspace.record_stream(stream)
-    _call("kvq_decode_kv", dev, stream, pq, _OUT_CODES[dtype], kv, p_table, block_table.shape[1], p_lens, softmax_scale,
-          num_splits, _on(workspace, "workspace", torch.uint8, dev), workspace.numel(), p_out, out_code, B, Hq, Hk, D, mods)
-    return out
+    return (_native_module or _native()).decode_kv(
+        q, k_cache, v_cache, block_table, seq_lens, softmax_scale, k_scale, v_scale, out, workspace, num_splits, out_dtype,
+        stream, sliding_window, softcap, sinks, alibi_slopes, lse_out)
 
 
 # ----------------------------------------------------------------------------------------------

@@ -252,14 +252,3 @@ def test_binding_refuses_cpu_tensors_and_wrong_types():
         kvq.kvq_write_kv(x, x, c, c, i.long())
     with pytest.raises(TypeError):
         kvq.kvq_plan_step(i, i, i[None], None, None, 16, 4, T=2)
-
-
-def test_packed_structs_are_the_ctypes_ones():
-    kv = kvq.PagedKv(1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 3, 12, 13)
-    assert kvq._pack_paged_kv(1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 3, 12, 13) == bytes(kv)
-    rot = kvq._pack_rotary(1, 2, 3, 4, 0.5)
-    assert len(rot) == ctypes.sizeof(kvq.Rotary) and rot[:28] == bytes(kvq.Rotary(1, 2, 3, 4, 0.5))[:28]
-    mods = kvq._pack_mods(1, 0.5, 3, 4, 5, 6, 7, 8)
-    assert len(mods) == ctypes.sizeof(kvq.ScoreMods)
-    got = kvq.ScoreMods.from_buffer_copy(mods)
-    assert [getattr(got, n) for n, _ in kvq.ScoreMods._fields_] == [1, 0.5, 3, 4, 5, 6, 7, 8]
