@@ -584,7 +584,6 @@ __global__ void __launch_bounds__(kKvThreads, 1) decode_kv_kernel(const __grid_c
   __shared__ volatile int s_failed;
   __shared__ long long s_scan[8], s_first_p;
   __shared__ int s_first_b;
-  asm volatile("griddepcontrol.launch_dependents;");  // let the merge kernel's launch begin early
   const SplitArgs &a = p.s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int W = a.warps_per_head, HB = a.heads_per_cta, CB = p.col_blocks;
@@ -597,6 +596,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) decode_kv_kernel(const __grid_c
     s_first_b = a.B;
     s_failed = 0;
   }
+  pdl_enter();
   __syncthreads();
 
   // ---- where the CTA's run starts
@@ -731,7 +731,8 @@ __global__ void __launch_bounds__(kKvThreads, 1) decode_kv_kernel(const __grid_c
 }
 
 // WPR warps for each output row (b, hq). Launched as a programmatic dependent of the split kernel: lengths and slot
-// ranges (recomputed for B <= 256, else from seg_first / seg_last) come before griddepcontrol.wait.
+// ranges (recomputed for B <= 256, else from seg_first / seg_last) come before the wait for it; they were written
+// before the split kernel started.
 template <int D, int WPR>
 __global__ void __launch_bounds__(256) kv_merge_kernel(const SplitArgs a) {
   constexpr int V = D / 32;
@@ -760,7 +761,7 @@ __global__ void __launch_bounds__(256) kv_merge_kernel(const SplitArgs a) {
     lo = static_cast<long long>(b) * a.num_splits;
     hi = lo + (sp.np + per - 1) / per;
   }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  pdl_enter();
   if (!scan && a.num_splits == 0 && sp.np > 0) {
     lo = static_cast<long long>(__ldcg(a.seg_first + b)) + b;
     hi = static_cast<long long>(__ldcg(a.seg_last + b)) + b + 1;
@@ -862,7 +863,9 @@ static kvq_status launch_kv(KvParams &p, int head_groups, const kvq_paged_kv *ca
   const size_t smem = static_cast<size_t>(p.slots) * slot + 1024;
   static size_t attr_done[kMaxDevices] = {};
   if (ensure_dynamic_smem(decode_kv_kernel<D, CT, NT, FOLD, MODS>, Gm::RING + 1024, attr_done) != cudaSuccess) return KVQ_ERR_CUDA;
-  decode_kv_kernel<D, CT, NT, FOLD, MODS><<<dim3(p.s.seg_ctas, head_groups), kKvThreads, smem, s>>>(p);
+  if (launch_dependent(decode_kv_kernel<D, CT, NT, FOLD, MODS>, dim3(p.s.seg_ctas, head_groups), dim3(kKvThreads), s, p, smem) !=
+      cudaSuccess)
+    return KVQ_ERR_CUDA;
   return launch_status();
 }
 
@@ -885,25 +888,12 @@ static kvq_status launch_kv_type(KvParams &p, int groups, const kvq_paged_kv *ca
 
 template <int D>
 static kvq_status launch_kv_merge(const KvParams &p, cudaStream_t s) {
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.blockDim = dim3(256);
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
   const long long rows = static_cast<long long>(p.s.B) * p.s.Hq;
   // partials of a row, on average: one warp reads 16 of them a round trip
   const long long parts = static_cast<long long>(p.s.num_splits > 0 ? p.s.num_splits : p.s.seg_ctas / p.s.B + 1) * p.s.warps_per_head;
-  cudaError_t e;
-  if (parts > 16) {
-    cfg.gridDim = dim3(static_cast<unsigned>(rows));
-    e = cudaLaunchKernelEx(&cfg, kv_merge_kernel<D, 8>, p.s);
-  } else {
-    cfg.gridDim = dim3(static_cast<unsigned>((rows + 7) / 8));
-    e = cudaLaunchKernelEx(&cfg, kv_merge_kernel<D, 1>, p.s);
-  }
+  const cudaError_t e =
+      parts > 16 ? launch_dependent(kv_merge_kernel<D, 8>, dim3(static_cast<unsigned>(rows)), dim3(256), s, p.s)
+                 : launch_dependent(kv_merge_kernel<D, 1>, dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256), s, p.s);
   return e == cudaSuccess ? launch_status() : KVQ_ERR_CUDA;
 }
 

@@ -176,6 +176,15 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return y;
 }
 
+// Start of a kernel that may be launched as a programmatic dependent of the one before it on its stream (any kernel):
+// wait until that one has finished and its writes are visible, then let the next launch begin -- in this order, so that
+// whatever the next kernel reads ahead of its own wait was finished before this kernel. Every CTA calls it: a grid that
+// could end without waiting would release its successor while its predecessor still runs.
+__device__ __forceinline__ void pdl_enter() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // ---------------------------------------------------------------------------------------------
 // mbarrier + TMA (cp.async.bulk.tensor) helpers
 // ---------------------------------------------------------------------------------------------

@@ -100,6 +100,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanArgs 
   __shared__ long long s_warp[3][kPlanThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   unsigned *report = blockIdx.x == 0 ? &g_flags_plan_step : nullptr;  // each fault once
+  pdl_enter();
 
   // a run of requests for each thread, their sums scanned over the block
   const int per = (a.B + kPlanThreads - 1) / kPlanThreads, b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
@@ -195,6 +196,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(const PlanArgs 
 // cursor advanced in place, behind the kernel that read it
 __global__ void __launch_bounds__(kPlanThreads) plan_advance_kernel(const PlanArgs a) {
   __shared__ long long s_warp[kPlanThreads / 32];
+  pdl_enter();
   long long n = 0;
   for (int b = threadIdx.x; b < a.B; b += kPlanThreads) {
     const Request r = load_request(a, b, nullptr);
@@ -282,8 +284,9 @@ extern "C" kvq_status kvq_plan_step(const int32_t *context_lens, const int32_t *
     static size_t attr_done[kMaxDevices] = {};
     if (ensure_dynamic_smem(plan_step_kernel, smem, attr_done) != cudaSuccess) return KVQ_ERR_CUDA;
   }
-  plan_step_kernel<<<static_cast<unsigned>(grid), kPlanThreads, smem, s>>>(a);
-  if (cudaGetLastError() != cudaSuccess) return KVQ_ERR_CUDA;
-  if (in_place && grid > 1) plan_advance_kernel<<<1, kPlanThreads, 0, s>>>(a);
+  if (launch_dependent(plan_step_kernel, dim3(static_cast<unsigned>(grid)), dim3(kPlanThreads), s, a, smem) != cudaSuccess)
+    return KVQ_ERR_CUDA;
+  if (in_place && grid > 1 && launch_dependent(plan_advance_kernel, dim3(1), dim3(kPlanThreads), s, a) != cudaSuccess)
+    return KVQ_ERR_CUDA;
   return launch_status();
 }

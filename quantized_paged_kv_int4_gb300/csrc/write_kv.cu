@@ -223,6 +223,7 @@ __global__ void __launch_bounds__(32 * kWriteWarps) write_kv_kernel(const WriteK
   constexpr int KOUT = POOL >= 0 ? POOL : IN;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int t = blockIdx.x * kWriteWarps + warp, part = blockIdx.y;
+  pdl_enter();
   if (t >= p.T) return;
   const bool rot = p.positions != nullptr;
   constexpr int EI = IN == KVQ_F32 ? 4 : 2, EK = POOL == kFp8Dst ? 1 : EI;
@@ -336,11 +337,10 @@ static kvq_status launch_write_kv(WriteKvParams &p, bool vec, cudaStream_t s) {
   const long long parts = want < most ? want : most;
   const size_t smem = p.positions != nullptr ? static_cast<size_t>(kWriteWarps) * p.half * sizeof(float2) : 0;
   const dim3 grid((p.T + kWriteWarps - 1) / kWriteWarps, static_cast<unsigned>(parts < 65535 ? parts : 65535));
-  if (vec)
-    write_kv_kernel<IN, POOL, true><<<grid, 32 * kWriteWarps, smem, s>>>(p);
-  else
-    write_kv_kernel<IN, POOL, false><<<grid, 32 * kWriteWarps, smem, s>>>(p);
-  return launch_status();
+  const dim3 block(32 * kWriteWarps);
+  const cudaError_t e = vec ? launch_dependent(write_kv_kernel<IN, POOL, true>, grid, block, s, p, smem)
+                            : launch_dependent(write_kv_kernel<IN, POOL, false>, grid, block, s, p, smem);
+  return e == cudaSuccess ? launch_status() : KVQ_ERR_CUDA;
 }
 
 static kvq_status check_rotary(const kvq_rotary *r, int D, WriteKvParams *p) {
