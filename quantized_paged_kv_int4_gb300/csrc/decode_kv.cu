@@ -45,7 +45,7 @@ namespace kvq {
 
 __device__ unsigned g_flags_decode_kv = 0;
 
-constexpr int kDirectPages = 8;
+constexpr int kDirectTiles = 4;
 constexpr float kSlack = 8.f;  // a weight is at most 2^8: fp16 keeps 2^-14 .. 2^8 at full precision
 
 struct KvParams {
@@ -173,10 +173,11 @@ struct KvRing {
 };
 
 // One worker, one piece: kv head h, query heads h G + 8 NT cb .. of it, pages sub, sub + W, ... of the piece. FOLD (G <= 4): columns 4 .. 7 repeat the
-// heads of columns 0 .. 3 and take the low parts of P. False when a wait on the ring ran out.
+// heads of columns 0 .. 3 and take the low parts of P. part_o, part_lse: the partial of the block's first head. False when a wait on the ring ran
+// out.
 template <int D, int CT, int NT, bool FOLD, bool MODS>
 __device__ __forceinline__ bool kv_piece(const KvParams &p, KvRing &rg, uint8_t *ring, const uint8_t *bad, int h, int cb,
-                                         int sub, const KvPiece &pc) {
+                                         int sub, const KvPiece &pc, float *part_o, float *part_lse) {
   using Gm = KvGeom<D, CT>;
   constexpr int MT = Gm::MT;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -440,7 +441,6 @@ __device__ __forceinline__ bool kv_piece(const KvParams &p, KvRing &rg, uint8_t 
 
   // ---- the piece's partial: lane (g, t) has columns 2t, 2t + 1 at two dims of each m-tile, 16 k + g and + 8 (FP8:
   // 16 k + 2g and + 1)
-  const long long row0 = (pc.slot * W + sub) * p.s.Hq + static_cast<long long>(h) * G;
   const float v_scale = CT == KV_E4M3 && p.v_scale != nullptr ? __ldg(p.v_scale + h) : 1.f;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
@@ -448,9 +448,9 @@ __device__ __forceinline__ bool kv_piece(const KvParams &p, KvRing &rg, uint8_t 
     for (int e = 0; e < 2; ++e) {
       const float sum = warp_sum_g(l[nt][e]);
       const float inv = sum > 0.f ? v_scale / sum : (sum == 0.f ? 0.f : sum);  // NaN stays
-      const int col = c0 + 8 * nt + 2 * t + e;
-      const bool owns = col < G && (!FOLD || t < 2);
-      float *dst = p.s.part_o + (row0 + (owns ? col : 0)) * D;
+      const int col = 8 * nt + 2 * t + e;
+      const bool owns = c0 + col < G && (!FOLD || t < 2);
+      float *dst = part_o + (owns ? col : 0) * D;
 #pragma unroll
       for (int k = 0; k < MT; ++k) {
         float x = acc[nt][k][e], y = acc[nt][k][e + 2];
@@ -467,7 +467,7 @@ __device__ __forceinline__ bool kv_piece(const KvParams &p, KvRing &rg, uint8_t 
           }
         }
       }
-      if (owns && g == 0) p.s.part_lse[row0 + col] = sum == 0.f ? -INFINITY : m[nt][e] + log2f(sum);
+      if (owns && g == 0) part_lse[col] = sum == 0.f ? -INFINITY : m[nt][e] + log2f(sum);
     }
   }
   return true;
@@ -584,6 +584,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) decode_kv_kernel(const __grid_c
   __shared__ volatile int s_failed;
   __shared__ long long s_scan[8], s_first_p;
   __shared__ int s_first_b;
+  __shared__ float s_lse[kKvWarps][8 * NT];  // direct: the workers' partials, s_part behind the ring
   const SplitArgs &a = p.s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int W = a.warps_per_head, HB = a.heads_per_cta, CB = p.col_blocks;
@@ -643,6 +644,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) decode_kv_kernel(const __grid_c
   rg.full = smem_u32(&s_full[0]);
   rg.empty = smem_u32(&s_empty[0]);
   rg.at = rg.phase = 0;
+  float *s_part = reinterpret_cast<float *>(kvq_kv_dsmem + off + rg.n * rg.stride);
   const int h0 = blockIdx.y / p.col_groups * HB, cg = blockIdx.y % p.col_groups;
   KvPiece pc;
 
@@ -706,7 +708,10 @@ __global__ void __launch_bounds__(kKvThreads, 1) decode_kv_kernel(const __grid_c
     rg.addr = dbase + mine;
     bool ok = true;
     while (ok && next_piece(a, cur, pc)) {
-      ok = kv_piece<D, CT, NT, FOLD, MODS>(p, rg, kvq_kv_dsmem + mine, s_bad, h0 + hl, cb, sub, pc);
+      const long long row = ((pc.slot * W + sub) * a.Hq + static_cast<long long>(h0 + hl) * a.G) + cb * 8 * NT;
+      ok = kv_piece<D, CT, NT, FOLD, MODS>(p, rg, kvq_kv_dsmem + mine, s_bad, h0 + hl, cb, sub, pc,
+                                           p.direct ? s_part + warp * 8 * NT * D : a.part_o + row * D,
+                                           p.direct ? &s_lse[warp][0] : a.part_lse + row);
       if (a.num_splits == 0 && tid == 0 && blockIdx.y == 0) {  // the sequence's first and last CTA, for the merge
         const SeqSpan sp = seq_span(a, pc.b, nullptr);
         if (pc.page == sp.f) a.seg_first[pc.b] = static_cast<int>(blockIdx.x);
@@ -715,16 +720,25 @@ __global__ void __launch_bounds__(kKvThreads, 1) decode_kv_kernel(const __grid_c
     }
     if (!ok && lane == 0) s_failed = 1;
   }
-  if (p.direct) {  // the partials of this CTA's sequence, joined here
+  if (p.direct) {  // the workers' partials of this CTA's sequence, joined here
     asm volatile("bar.sync 1, 256;" ::: "memory");
+    constexpr int V = D / 32, COLS = 8 * NT;
     const int b = blockIdx.x;
-    const long long lo = static_cast<long long>(b) * W, hi = seq_span(a, b, nullptr).np > 0 ? lo + W : lo;
-    const int cols = CB * 8 * NT;
-    for (int i = warp; i < HB * cols; i += kKvWarps) {
-      const int col = cg * cols + i % cols, hq = (h0 + i / cols) * a.G + col;
+    const bool empty = seq_span(a, b, nullptr).np == 0;
+    for (int i = warp; i < HB * CB * COLS; i += kKvWarps) {
+      const int group = i / COLS, col = (cg * CB + group % CB) * COLS + i % COLS, hq = (h0 + group / CB) * a.G + col;
       if (col >= a.G) continue;
-      float M, den, o[D / 32];
-      kv_join<D>(a, hq, lo, hi, 1, lane, M, den, o);
+      float M = -INFINITY, den = 0.f, o[V];
+#pragma unroll
+      for (int j = 0; j < V; ++j) o[j] = 0.f;
+      for (int s = 0; s < W && !empty; ++s) M = fmaxf(M, s_lse[s * HB * CB + group][i % COLS]);
+      for (int s = 0; s < W && !empty; ++s) {
+        const int w = s * HB * CB + group;
+        const float lse = s_lse[w][i % COLS], f = lse == -INFINITY ? 0.f : exp2f(lse - M);
+        den += f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) o[j] = fmaf(f, s_part[(w * COLS + i % COLS) * D + lane * V + j], o[j]);
+      }
       kv_finish<D>(a, b, hq, lane, kv_sink2(a, hq), M, den, o);
     }
   }
@@ -818,6 +832,11 @@ static int kv_wave(int ctas, int head_groups) { return head_groups < ctas ? ctas
 struct KvPlan {
   int HB, CB, W, col_groups, head_groups, grid_x;
   long long slots;  // of W partials for each query head
+  void set_heads(int hb, int Hk) {
+    HB = hb;
+    W = kKvWarps / (hb * CB);
+    head_groups = Hk / hb * col_groups;
+  }
 };
 static bool kv_plan(int B, int Hq, int Hk, int D, int num_splits, KvPlan *plan) {
   const int G = Hq / Hk, cols = 8 * kv_tiles(G, D), blocks = (G + cols - 1) / cols;
@@ -825,11 +844,8 @@ static bool kv_plan(int B, int Hq, int Hk, int D, int num_splits, KvPlan *plan) 
   plan->CB = (blocks + plan->col_groups - 1) / plan->col_groups;
   int hb = kKvWarps;
   while (hb * plan->CB > kKvWarps || Hk % hb) hb /= 2;
-  plan->HB = hb;
-  plan->W = kKvWarps / (hb * plan->CB);
-  const long long groups = static_cast<long long>(Hk / hb) * plan->col_groups;
-  if (groups > 65535) return false;
-  plan->head_groups = static_cast<int>(groups);
+  if (static_cast<long long>(Hk) * plan->col_groups > 65535) return false;
+  plan->set_heads(hb, Hk);
   if (num_splits > 0) {
     const long long ctas = static_cast<long long>(B) * num_splits;
     if (ctas > 0x7fffffffLL) return false;
@@ -858,9 +874,10 @@ static kvq_status launch_kv(KvParams &p, int head_groups, const kvq_paged_kv *ca
       !paged_tensor_map(cache->v, Gm::ROW, Gm::PB, HB, cache->v_stride_token * es, cache->v_stride_head * es,
                         cache->v_stride_block * es, p.bs, p.s.Hk, cache->num_blocks, &p.v))
     return KVQ_ERR_CUDA;
-  const int slot = p.s.warps_per_head * HB * Gm::HALF, fit = Gm::RING / slot;
+  const int slot = p.s.warps_per_head * HB * Gm::HALF, parts = p.direct ? kKvWarps * 8 * NT * D * 4 : 0;
+  const int fit = (Gm::RING - parts) / slot;
   p.slots = fit < kKvMaxSlots ? fit : kKvMaxSlots;
-  const size_t smem = static_cast<size_t>(p.slots) * slot + 1024;
+  const size_t smem = static_cast<size_t>(p.slots) * slot + parts + 1024;
   static size_t attr_done[kMaxDevices] = {};
   if (ensure_dynamic_smem(decode_kv_kernel<D, CT, NT, FOLD, MODS>, Gm::RING + 1024, attr_done) != cudaSuccess) return KVQ_ERR_CUDA;
   if (launch_dependent(decode_kv_kernel<D, CT, NT, FOLD, MODS>, dim3(p.s.seg_ctas, head_groups), dim3(kKvThreads), s, p, smem) !=
@@ -949,21 +966,30 @@ extern "C" kvq_status kvq_decode_kv(const void *q, kvq_dtype q_dtype, const kvq_
   sa.Hk = Hk;
   sa.G = Hq / Hk;
   sa.Q = 1;
-  sa.heads_per_cta = plan.HB;
-  sa.warps_per_head = plan.W;
   sa.slots = plan.slots;
-  // One CTA for each sequence and head group, one launch: asked for by num_splits = 1, or where the tables allow at most
-  // kDirectPages pages for each worker.
-  p.direct = num_splits == 1 ||
-             (num_splits == 0 && B <= plan.grid_x && sa.max_blocks <= static_cast<long long>(kDirectPages) * plan.W);
-  if (p.direct) sa.num_splits = 1;
-  sa.seg_ctas = p.direct ? B : plan.grid_x;
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   const size_t part_rows = static_cast<size_t>(plan.slots) * plan.W * Hq;
   sa.part_o = reinterpret_cast<float *>(ws);
   sa.part_lse = reinterpret_cast<float *>(ws += round256(part_rows * D * sizeof(float)));
   sa.seg_first = reinterpret_cast<int32_t *>(ws += round256(part_rows * sizeof(float)));
   sa.seg_last = reinterpret_cast<int32_t *>(ws + round256(static_cast<size_t>(B) * sizeof(int32_t)));
+  // One CTA for each sequence and head group, one launch, nothing through the workspace: asked for by num_splits = 1, or
+  // where one wave of CTAs, of as few heads (as many pages at a time) as that allows, has at most kDirectTiles tiles
+  // a worker.
+  p.direct = num_splits == 1;
+  for (int hb = 1; num_splits == 0 && !p.direct && hb <= plan.HB; hb *= 2) {
+    KvPlan d = plan;
+    d.set_heads(hb, Hk);
+    if (static_cast<long long>(B) * d.head_groups <= sm_count()) {
+      p.direct = sa.max_blocks <= static_cast<long long>(kDirectTiles) * d.W;
+      if (p.direct) plan = d;
+      break;
+    }
+  }
+  if (p.direct) sa.num_splits = 1;
+  sa.seg_ctas = p.direct ? B : plan.grid_x;
+  sa.heads_per_cta = plan.HB;
+  sa.warps_per_head = plan.W;
   sa.out = out;
   sa.out_dtype = out_dtype;
   sa.window = mods ? mods->sliding_window : 0;

@@ -296,13 +296,13 @@ def test_binding_checks():
 
 
 @pytest.mark.parametrize("cache,D", [(BF, 128), (E4, 64), (F16, 256)])
-@pytest.mark.parametrize("stage", [0, 1, 2])
-def test_bounded_wait_is_flagged_and_the_next_call_is_exact(cache, D, stage):
+@pytest.mark.parametrize("stage,S", [(0, 1), (1, 1), (0, 2), (2, 2)])
+def test_bounded_wait_is_flagged_and_the_next_call_is_exact(cache, D, stage, S):
     """A copy that never comes (withheld on the host's order, nothing faults): flag 8, and the context goes on."""
     c = Case([700, 33, 100], 8, 2, D, cache, seed=15)
     kvq.kvq_debug_set_wait(5_000_000, stage)
     try:
-        c.run(num_splits=1)  # the first CTA has all of sequence 0: its first warp goes round its ring
+        c.run(num_splits=S)  # the first CTA's run of sequence 0 goes through the ring slot
         assert kvq.kvq_device_error() == (kvq.KVQ_ERR_OUT_OF_RANGE, 8)
     finally:
         kvq.kvq_debug_set_wait(0, -1)
