@@ -415,7 +415,7 @@ KVQ_API kvq_status kvq_fwht128(const void *x, uint8_t *y_e4m3, float *row_scale,
  * Rows of positions and slot_mapping behind the last token are set to -1, which every write skips.
  *
  *   context_lens  int32 [B].   query_lens  int32 [B], or NULL: one new token each.
- *   rows          int32 [B], all different, or NULL: request b is row b.
+ *   rows          int32 [B], all different (two requests with one row race: caller error), or NULL: row b.
  *   block_table   int32 [num_rows, max_blocks], extended in place.
  *   free_blocks   int32 [num_free], ids in the order they are handed out, with cursor int64 [1]; or
  *                 NULL (cursor and cursor_out NULL too): the table already holds every block.
@@ -498,7 +498,8 @@ KVQ_API kvq_status kvq_rope(const void *q, int64_t q_stride_t, int64_t q_stride_
  * kvq_paged_kv -- a paged cache of keys and values in 16 bits or FP8 E4M3FN.
  *   k, v       element (block, row, head, d) at ptr + block*stride_block + row*stride_token +
  *              head*stride_head + d: [num_blocks, block_size, Hk, D], K and V in one pool, or the head
- *              before the token, as the strides say. Base 16-byte aligned; strides >= 0 and multiples of 16 bytes.
+ *              before the token, as the strides say. Base 16-byte aligned; strides multiples of 16 bytes,
+ *              > 0 (a dimension of one element: any).
  *   k_scale, v_scale  fp32 [Hk] each or NULL (1): an FP8 code c of head h stands for c * scale[h].
  *              NULL for 16-bit caches.
  *   dtype      KVQ_BF16, KVQ_F16 or KVQ_E4M3.
@@ -525,7 +526,8 @@ typedef struct kvq_paged_kv {
  *
  *   key, value    [T, Hk, D] of dtype (KVQ_BF16 or KVQ_F16; a 16-bit cache has the same type), strides as
  *                 kvq_write_int4: base 16-byte aligned, strides multiples of 8 elements.
- *   slot_mapping  int64 [T]; entries < 0 are skipped, entries >= num_blocks*block_size skipped and flagged (4).
+ *   slot_mapping  int64 [T]; entries < 0 are skipped, entries >= num_blocks*block_size skipped and flagged (4). Two
+ *                 tokens with the same slot race (caller error).
  *   q, q_out      as kvq_rope, same alignment rules as key; NULL with Hq == 0. Needs rotary.
  *   D             a multiple of 8, at most 256. block_size >= 1.
  */
@@ -555,7 +557,10 @@ KVQ_API kvq_status kvq_write_kv(const void *key, int64_t k_stride_t, int64_t k_s
  *   mods          NULL or as kvq_decode_int4_mods; single-token only (q_len > 1 or query_start_loc:
  *                 KVQ_ERR_UNSUPPORTED).
  *   Supported: D in {64, 128, 256}; block_size a multiple of 16; any Hk, any Hq / Hk.
- * Contents of the cache behind a sequence's end, and of blocks no table names, may be anything (NaN included).
+ * Contents of the cache behind a sequence's end, and of blocks no table names, may be anything (NaN included). Over an
+ * FP8 cache a query element beyond ~2^100, or not finite, raises flag 16.
+ * Sums are fp32; weights enter the products with a relative error of at most 2^-16 (2^-11 over an FP8 cache with more than
+ * 8 query heads a kv head). The same bits whatever else runs; num_splits changes the order of the sums.
  */
 KVQ_API size_t kvq_decode_kv_workspace_bytes(int32_t B, int32_t Hq, int32_t Hk, int32_t D, int32_t num_splits);
 
@@ -582,13 +587,13 @@ KVQ_API kvq_status kvq_copy_async(void *dst, const void *src, size_t bytes, kvq_
 
 /*
  * kvq_debug_set_wait -- for tests of the error path only (no counterpart on the pages).
- * Every wait of the decode kernels (INT4 and TurboQuant) on a page copy is bounded; when one runs
+ * Every wait of the decode kernels (INT4, TurboQuant and kvq_decode_kv) on a page copy is bounded; when one runs
  * out the kernel raises flag 8, lets the copies it has issued land, and returns, so the context
  * stays usable. This call makes that path reachable on purpose, without any fault:
  *   wait_limit_ns   the limit of every such wait from now on in this process (0: the default, 2 s).
- *   withhold_stage  >= 0: the NEXT decode call (kvq_decode_int4, _int4_mods, _tq, _tq_lse or
- *                   _tq_mse; that one call only) does not issue the copies of that ring stage in
- *                   its first CTA (TurboQuant: of that ring tile of the CTA's first warp), so the
+ *   withhold_stage  >= 0: the NEXT decode call (kvq_decode_int4, _int4_mods, _tq, _tq_lse, _tq_mse
+ *                   or kvq_decode_kv; that one call only) does not issue the copies of that ring stage in
+ *                   its first CTA (TurboQuant: of that ring tile of the CTA's first warp; kvq_decode_kv: of that ring slot), so the
  *                   wait on it runs out after wait_limit_ns (plus ~0.1 s for the bounded drain) and
  *                   flag 8 is raised; that call's results are not valid. -1: none.
  * Returns KVQ_ERR_INVALID_ARG for withhold_stage < -1.

@@ -230,6 +230,10 @@ kvq_status check_paged_kv(const kvq_paged_kv *c, kvq_dtype dtype) {
   for (int64_t st : {c->k_stride_block, c->k_stride_token, c->k_stride_head, c->v_stride_block, c->v_stride_token,
                      c->v_stride_head})
     if (st < 0 || st % unit) return KVQ_ERR_INVALID_ARG;
+  // rows and blocks of their own (a dimension of one element may come with any stride)
+  if ((c->block_size > 1 && (c->k_stride_token == 0 || c->v_stride_token == 0)) ||
+      (c->num_blocks > 1 && (c->k_stride_block == 0 || c->v_stride_block == 0)))
+    return KVQ_ERR_INVALID_ARG;
   return KVQ_OK;
 }
 

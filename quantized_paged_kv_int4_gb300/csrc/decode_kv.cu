@@ -184,9 +184,10 @@ struct KvRing {
   }
 };
 
-// One worker, one piece: kv head h, query heads h G + 8 NT cb .. of it, pages sub, sub + W, ... of the piece. FOLD (G <= 4): columns 4 .. 7 repeat the
-// heads of columns 0 .. 3 and take the low parts of P. part_o, part_lse: the partial of the block's first head. False when a wait on the ring ran
-// out.
+// One worker, one piece: kv head h, query heads h G + 8 NT cb .. of it, pages sub, sub + W, ... of the piece. FOLD
+// (G <= 4): columns 4 .. 7 repeat the heads of columns 0 .. 3 and take the low parts of P. part_o, part_lse: the
+// partial of the block's first head. False when a wait on the ring ran out. (Every worker waits for every entry of the
+// ring, its own or not: a wait by parity is only right for one who saw the phase before.)
 template <int D, int CT, int NT, bool FOLD, bool MODS>
 __device__ __forceinline__ bool kv_piece(const KvParams &p, KvRing &rg, uint8_t *ring, const uint32_t *bad, int h, int cb,
                                          int sub, const KvPiece &pc, float *part_o, float *part_lse) {

@@ -1,8 +1,8 @@
 """kvq_decode_kv against the float64 oracle on the values the cache holds.
 
 Bound of an output element o = sum p v, with A = sum p |v| (weights p that sum to at most 1):
-  the weights enter the product with a relative error of 2^-11 (fp16; fp16 and FP8 caches) or 2^-16 (bf16 in two
-  parts); scores are sums of D exact products in fp32 and lie below 2^5 here, an error below 2^-14; the exponential,
+  the weights enter the product with a relative error of at most 2^-11 (FP8 caches, one rounding to fp16) or 2^-16 (in
+  two parts); scores are sums of D exact products in fp32 and lie below 2^5 here, an error below 2^-14; the exponential,
   the sums over a few hundred tiles and the joining add less than 2^-13: (w + 2^-12) A in all; and half a step of the
   output's type, eps / 2 |o|.
 Bound of the log-sum-exp: the scores' error and fp32 roundings of a value below 2^5: 1e-4."""
@@ -85,7 +85,7 @@ class Case:
         mods = {n: x for n, x in kw.items() if n in ("sliding_window", "softcap", "sinks", "alibi_slopes")}
         ref, ref_lse, size = want or self.oracle(**mods)
         err = np.abs(f64(out) - ref)
-        w = 2.0 ** -16 if self.cache == BF else 2.0 ** -11
+        w = 2.0 ** -11 if self.cache == E4 else 2.0 ** -16
         bound = (w + 2.0 ** -12) * size + (torch.finfo(out.dtype).eps / 2 if out.dtype != F32 else 0) * np.abs(ref) * 1.01 + 1e-7
         assert (err <= bound).all(), "%g times the bound" % np.nanmax(np.where(err <= bound, 0, err / bound))
         got = f64(lse)
@@ -207,6 +207,27 @@ def test_scores_of_minus_infinity():
     assert not np.array_equal(ref[0][0], clean[0][0])
 
 
+@pytest.mark.parametrize("cache", [BF, E4])
+@pytest.mark.parametrize("Hq,Hk,D", [(136, 1, 64), (72, 1, 256), (400, 2, 64), (48, 2, 128), (20, 4, 256)])
+def test_many_query_heads(Hq, Hk, D, cache):
+    """More blocks of query heads than a CTA has workers, and numbers of blocks that do not fill it."""
+    c = Case([0, 33, 700, 16, 1], Hq, Hk, D, cache, seed=Hq)
+    want = c.oracle()
+    for S in (0, 1, 3):
+        c.check(want, num_splits=S)
+
+
+@pytest.mark.parametrize("cache", [BF, F16, E4])
+@pytest.mark.parametrize("Hq,Hk,D", [(8, 8, 64), (16, 8, 128), (30, 5, 256), (4, 1, 128), (16, 1, 64), (24, 1, 256)])
+def test_rings_go_round_many_times(Hq, Hk, D, cache):
+    """Long runs: every ring slot is used many times, with pieces that end inside a slot."""
+    c = Case([9001, 4099, 17, 6000], Hq, Hk, D, cache, bs=32, layout="paired", seed=D)
+    want = c.oracle()
+    for S in (0, 1, 2):
+        c.check(want, num_splits=S)
+    c.check(sliding_window=4096, softcap=30.0)
+
+
 def test_long_sequence_split():
     c = Case([50001, 3], 8, 1, 64, F16, seed=10)
     want = c.oracle()
@@ -276,6 +297,22 @@ def test_repeatable_and_on_another_stream_and_captured():
     assert not torch.equal(outs[0], outs[2])
     c.lens.clamp_(max=1)
     c.check()
+
+
+def test_calls_at_once_on_two_streams():
+    """Two batches on two streams, several times, each with a workspace of its own: the bits of the calls alone."""
+    cases = [Case([3000, 77, 1024], 8, 2, 128, BF, seed=21), Case([900, 4000], 16, 8, 64, E4, seed=22)]
+    alone = [c.run()[0].clone() for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    args = [dict(q=c.q.cuda(), k_cache=c.k, v_cache=c.v, block_table=c.table.cuda(), seq_lens=c.lens.cuda(), softmax_scale=c.scale,
+                 k_scale=None if c.k_scale is None else c.k_scale.cuda(), v_scale=None if c.v_scale is None else c.v_scale.cuda())
+            for c in cases]
+    torch.cuda.synchronize()
+    outs = [[kvq.kvq_decode_kv(stream=s, **a) for a, s in zip(args, streams)] for _ in range(20)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for pair in outs for o, want in zip(pair, alone))
+    assert kvq.kvq_device_error() == (0, 0)
 
 
 def test_binding_checks():

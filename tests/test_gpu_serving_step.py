@@ -68,7 +68,7 @@ def test_prefill_then_decode(cache, bs, Hq, Hk, D):
                 low = 0 if s is None else float(s[0]) * 2.0 ** -10
                 assert (np.abs(got - made) <= torch.finfo(cache).eps / 2 * np.abs(made) * 1.001 + 1e-5 + low).all()
         ref, _, size = paged_kv.decode(f64(q_out[last]), ko, vo, t, lens.tolist(), D ** -0.5)
-        w = 2.0 ** -16 if cache == BF else 2.0 ** -11
+        w = 2.0 ** -11 if cache == E4 else 2.0 ** -16
         bound = (w + 2.0 ** -12) * size + torch.finfo(dtype).eps / 2 * np.abs(ref) * 1.01 + 1e-7
         assert (np.abs(f64(out) - ref) <= bound).all(), step
 

@@ -179,7 +179,8 @@ def _kv(**kw):
 
 BAD_CACHES = (dict(k=None), dict(v=None), dict(k=24), dict(v=24), dict(kb=2052), dict(kt=-128), dict(vh=4), dict(bs=0),
               dict(nb=0), dict(dtype=2), dict(dtype=7), dict(dtype=1), dict(ks=16), dict(vs=16),
-              dict(dtype=3, kt=136), dict(dtype=3, ks=18))
+              dict(dtype=3, kt=136), dict(dtype=3, ks=18),
+              dict(kt=0), dict(vt=0), dict(kb=0), dict(vb=0))
 
 
 def _write(**kw):
