@@ -183,7 +183,7 @@ bool tq_tensor_map(const void *cache, long long num_blocks, int Hk, int slot_byt
   return true;
 }
 
-bool paged_tensor_map(const void *base, int row_bytes, int part_bytes, int box_heads, long long token, long long head, long long block,
+bool paged_tensor_map(const void *base, int row_bytes, int part_bytes, int box_parts, int box_heads, long long token, long long head, long long block,
                       int block_size, int Hk, long long num_blocks, CUtensorMap *map) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = encode_tiled();
   if (enc == nullptr) return false;
@@ -194,7 +194,8 @@ bool paged_tensor_map(const void *base, int row_bytes, int part_bytes, int box_h
   const cuuint64_t stride[4] = {static_cast<cuuint64_t>(token), static_cast<cuuint64_t>(part_bytes),
                                 static_cast<cuuint64_t>(Hk > 1 ? head : row_bytes),
                                 static_cast<cuuint64_t>(num_blocks > 1 ? block : row_bytes)};
-  const cuuint32_t box[5] = {static_cast<cuuint32_t>(part_bytes), 16, static_cast<cuuint32_t>(parts), static_cast<cuuint32_t>(box_heads), 1};
+  const cuuint32_t box[5] = {static_cast<cuuint32_t>(part_bytes), 16, static_cast<cuuint32_t>(box_parts),
+                             static_cast<cuuint32_t>(box_heads), 1};
   const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, const_cast<void *>(base), dim, stride, box, ones,
              CU_TENSOR_MAP_INTERLEAVE_NONE, part_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,

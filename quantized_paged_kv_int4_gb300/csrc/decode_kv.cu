@@ -92,6 +92,10 @@ struct KvGeom {  // HALF: K or V of one (page, kv head)
   // Scores of the next step ahead of this step's weights, where the ring has slots to spare (it holds K of the next and V of
   // this step).
   static constexpr bool AHEAD = ROW < 512 && NT == 1;
+  // Ring entries of a tile's K (and V): the largest tiles come in two halves of the row, so that the ring has six slots
+  // and not three (16 sequences of 4096 bf16 tokens, D = 256, 8 kv heads: 89 -> 87 us).
+  static constexpr int H = ROW == 512 ? 2 : 1;
+  static constexpr int ENTRY = HALF / H;
   static constexpr int RING = 216 * 1024;                  // bytes of the ring
 };
 
@@ -192,7 +196,7 @@ template <int D, int CT, int NT, bool FOLD, bool MODS>
 __device__ __forceinline__ bool kv_piece(const KvParams &p, KvRing &rg, uint8_t *ring, const uint32_t *bad, int h, int cb,
                                          int sub, const KvPiece &pc, float *part_o, float *part_lse) {
   using Gm = KvGeom<D, CT, NT>;
-  constexpr int MT = Gm::MT, U = Gm::U;
+  constexpr int MT = Gm::MT, U = Gm::U, H = Gm::H;
   constexpr bool AHEAD = Gm::AHEAD;
   constexpr bool LOW = !FOLD && (CT != KV_E4M3 || NT == 1);  // the low parts of P in a product of their own
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -290,49 +294,51 @@ __device__ __forceinline__ bool kv_piece(const KvParams &p, KvRing &rg, uint8_t 
     return (base ^ ((2 * c2 % CP) << 4)) + (2 * c2 / CP) * (kPage * Gm::PB);
   };
 
-  // Scores of a tile, from its K: rows are tokens g, g + 8, columns 2t, 2t + 1; in several chains of products
-  auto scores = [&](uint32_t tile, float (&out)[NT][4]) {
+  // Scores of a tile, from the hh-th of the H parts of its K: rows are tokens g, g + 8, columns 2t, 2t + 1; in NC chains
+  constexpr int NC = NT == 1 && MT >= 8 ? 4 : 2, MH = MT / H;
+  struct Chains {
+    float c[NC][NT][4];
+  };
+  auto scores = [&](uint32_t tile, int hh, Chains &S) {
     const uint32_t ka = tile + k_lane;
-    constexpr int NC = NT == 1 && MT >= 8 ? 4 : 2;
-    float S[NC][NT][4];
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) S[c][nt][0] = S[c][nt][1] = S[c][nt][2] = S[c][nt][3] = 0.f;
-    }
     if constexpr (CT != KV_E4M3) {
 #pragma unroll
-      for (int ks = 0; ks < MT; ++ks) {
+      for (int ks = 0; ks < MH; ++ks) {
         uint32_t a[4];
         ldmatrix4(chunk_at(ka, ks), a);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_kv<CT>(S[ks % NC][nt], a[0], a[1], a[2], a[3], qf[nt][ks][0], qf[nt][ks][1]);
+        for (int nt = 0; nt < NT; ++nt)
+          mma_kv<CT>(S.c[ks % NC][nt], a[0], a[1], a[2], a[3], qf[nt][hh * MH + ks][0], qf[nt][hh * MH + ks][1]);
       }
     } else {
 #pragma unroll
-      for (int k2 = 0; k2 < MT / 2; ++k2) {
+      for (int k2 = 0; k2 < MH / 2; ++k2) {
         uint32_t r[4];
         ldmatrix4(chunk_at(ka, k2), r);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
+          const int ks = 2 * k2 + u;
           uint32_t a0, a1, a2, a3;
           e4m3x4_f16x4(r[2 * u], a0, a2);
           e4m3x4_f16x4(r[2 * u + 1], a1, a3);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma_kv<CT>(S[(2 * k2 + u) % NC][nt], a0, a1, a2, a3, qf[nt][2 * k2 + u][0], qf[nt][2 * k2 + u][1]);
+          for (int nt = 0; nt < NT; ++nt)
+            mma_kv<CT>(S.c[ks % NC][nt], a0, a1, a2, a3, qf[nt][hh * MH + ks][0], qf[nt][hh * MH + ks][1]);
         }
       }
     }
+  };
+  auto sum_of = [&](const Chains &S, float (&out)[NT][4]) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        out[nt][e] = NC == 4 ? (S[0][nt][e] + S[1][nt][e]) + (S[2][nt][e] + S[NC - 1][nt][e]) : S[0][nt][e] + S[1][nt][e];
+        out[nt][e] = NC == 4 ? (S.c[0][nt][e] + S.c[1][nt][e]) + (S.c[2][nt][e] + S.c[NC - 1][nt][e]) : S.c[0][nt][e] + S.c[1][nt][e];
     }
   };
-  // Ring entries come K, V, K, V, ...: a step takes U tiles from one of each. AHEAD: K of the next step together with V of
+  // Ring entries come K, V, K, V, ... (H = 2: two of K, two of V): a step takes U tiles from each. AHEAD: K of the next step together with V of
   // this one, so that the next scores are on the tensor cores while this step's weights are computed.
-  KvRing rk = rg, rv = rg;
+  KvRing rk = rg, rv = rg;  // AHEAD: the next K and V; else rg is the one place
   rv.advance();
   const int per = U * W, steps = (pc.n + per - 1) / per;
   const uint32_t tile_step = rg.stride / U;  // from a worker's tile to its next in the slot
@@ -343,7 +349,11 @@ __device__ __forceinline__ bool kv_piece(const KvParams &p, KvRing &rg, uint8_t 
   uint32_t bad_now = 0, bad_next = 0;  // pages of the slot without a block of their own
   auto scores_of = [&](const KvRing &r, float (&out)[U][NT][4], uint32_t &no_block) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) scores(rg.addr + r.at * rg.stride + u * tile_step, out[u]);
+    for (int u = 0; u < U; ++u) {
+      Chains S = {};
+      scores(rg.addr + r.at * rg.stride + u * tile_step, 0, S);
+      sum_of(S, out[u]);
+    }
     no_block = bad[r.at];
   };
   if (AHEAD && sub < pc.n) {
@@ -358,15 +368,23 @@ __device__ __forceinline__ bool kv_piece(const KvParams &p, KvRing &rg, uint8_t 
     const int i0 = st * per + sub;  // the worker's tiles: pages i0 + u W of the piece
     const bool mine = i0 < pc.n;
     if (!mine) {  // the run ends inside the slot: nothing of this worker's
-      if (!AHEAD || st == 0) {
-        if (!landed(rk)) return false;
-        release(rk);
+      if constexpr (AHEAD) {
+        if (st == 0) {
+          if (!landed(rk)) return false;
+          release(rk);
+        }
+        if (!landed(rv)) return false;
+        release(rv);
+        rv.advance();
+        rg.at = rv.at;
+        rg.phase = rv.phase;
+      } else {
+        for (int e = 0; e < 2 * H; ++e) {
+          if (!landed(rg)) return false;
+          release(rg);
+          rg.advance();
+        }
       }
-      if (!landed(rv)) return false;
-      release(rv);
-      rv.advance();
-      rg.at = rv.at;
-      rg.phase = rv.phase;
       break;
     }
     const bool more = st + 1 < steps;
@@ -374,10 +392,19 @@ __device__ __forceinline__ bool kv_piece(const KvParams &p, KvRing &rg, uint8_t 
       if (!landed(rv) || (more && !landed(rk))) return false;
       scores_of(rk, Sn, bad_next);  // without a next step: of whatever is there, unused
     } else {
-      if (!landed(rk)) return false;
-      scores_of(rk, Sc, bad_now);
-      __syncwarp();
-      release(rk);
+      Chains S[U] = {};
+#pragma unroll
+      for (int hh = 0; hh < H; ++hh) {
+        if (!landed(rg)) return false;
+#pragma unroll
+        for (int u = 0; u < U; ++u) scores(rg.addr + rg.at * rg.stride + u * tile_step, hh, S[u]);
+        if (hh == 0) bad_now = bad[rg.at];
+        __syncwarp();
+        release(rg);
+        rg.advance();
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) sum_of(S[u], Sc[u]);
     }
     int lo[U], hi[U];  // live tokens of the tiles
     bool partial = false;  // warp-uniform
@@ -478,67 +505,76 @@ __device__ __forceinline__ bool kv_piece(const KvParams &p, KvRing &rg, uint8_t 
       }
     }
     // ---- O^T += V^T P^T
-    if constexpr (!AHEAD) {
-      if (!landed(rv)) return false;
-    }
-    const uint32_t vt = rg.addr + rv.at * rg.stride;
-    if (partial) {  // values of dead tokens may be anything: zero them (0 * NaN is NaN)
+    const KvRing &rvr = AHEAD ? rv : rg;
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        uint8_t *vs = ring + rv.at * rg.stride + u * tile_step;
-        for (int c = lane; c < Gm::HALF / 16; c += 32) {
-          const int row = c / CP % kPage;
-          if (row < lo[u] || row >= hi[u]) *reinterpret_cast<uint4 *>(vs + 16 * c) = make_uint4(0, 0, 0, 0);
-        }
+    for (int hh = 0; hh < H; ++hh) {
+      if constexpr (!AHEAD) {
+        if (!landed(rvr)) return false;
       }
-      fence_proxy_async();
-      __syncwarp();
-    }
-    if constexpr (CT != KV_E4M3) {
-#pragma unroll
-      for (int k = 0; k < MT; ++k) {
+      const uint32_t vt = rg.addr + rvr.at * rg.stride;
+      if (partial) {  // values of dead tokens may be anything: zero them (0 * NaN is NaN)
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          uint32_t a[4];
-          ldmatrix4_trans(chunk_at(vt + u * tile_step + v_lane, k), a);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma_kv<CT>(acc[nt][k], a[0], a[1], a[2], a[3], ph[u][nt][0], ph[u][nt][1]);
-            if constexpr (LOW) mma_kv<CT>(acc[nt][k], a[0], a[1], a[2], a[3], pl[u][nt][0], pl[u][nt][1]);
+          uint8_t *vs = ring + rvr.at * rg.stride + u * tile_step;
+          for (int c = lane; c < Gm::ENTRY / 16; c += 32) {
+            const int row = c / CP % kPage;
+            if (row < lo[u] || row >= hi[u]) *reinterpret_cast<uint4 *>(vs + 16 * c) = make_uint4(0, 0, 0, 0);
           }
         }
+        fence_proxy_async();
+        __syncwarp();
       }
-    } else {
+      if constexpr (CT != KV_E4M3) {
 #pragma unroll
-      for (int k2 = 0; k2 < MT / 2; ++k2) {
+        for (int k = 0; k < MH; ++k) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          uint32_t r[4];
-          ldmatrix4_trans(chunk_at(vt + u * tile_step + v_lane, k2), r);
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {  // dims 16 (2 k2 + x) + 2g, + 1
-            uint32_t a0, a1, a2, a3;
-            e4m3x4_f16x4(__byte_perm(r[x], 0, 0x3120), a0, a1);
-            e4m3x4_f16x4(__byte_perm(r[x + 2], 0, 0x3120), a2, a3);
+          for (int u = 0; u < U; ++u) {
+            uint32_t a[4];
+            ldmatrix4_trans(chunk_at(vt + u * tile_step + v_lane, k), a);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              mma_kv<CT>(acc[nt][2 * k2 + x], a0, a1, a2, a3, ph[u][nt][0], ph[u][nt][1]);
-              if constexpr (LOW) mma_kv<CT>(acc[nt][2 * k2 + x], a0, a1, a2, a3, pl[u][nt][0], pl[u][nt][1]);
+              mma_kv<CT>(acc[nt][hh * MH + k], a[0], a[1], a[2], a[3], ph[u][nt][0], ph[u][nt][1]);
+              if constexpr (LOW) mma_kv<CT>(acc[nt][hh * MH + k], a[0], a[1], a[2], a[3], pl[u][nt][0], pl[u][nt][1]);
+            }
+          }
+        }
+      } else {
+#pragma unroll
+        for (int k2 = 0; k2 < MH / 2; ++k2) {
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            uint32_t r[4];
+            ldmatrix4_trans(chunk_at(vt + u * tile_step + v_lane, k2), r);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {  // dims 16 (2 k2 + x) + 2g, + 1
+              uint32_t a0, a1, a2, a3;
+              e4m3x4_f16x4(__byte_perm(r[x], 0, 0x3120), a0, a1);
+              e4m3x4_f16x4(__byte_perm(r[x + 2], 0, 0x3120), a2, a3);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                mma_kv<CT>(acc[nt][hh * MH + 2 * k2 + x], a0, a1, a2, a3, ph[u][nt][0], ph[u][nt][1]);
+                if constexpr (LOW) mma_kv<CT>(acc[nt][hh * MH + 2 * k2 + x], a0, a1, a2, a3, pl[u][nt][0], pl[u][nt][1]);
+              }
             }
           }
         }
       }
+      if constexpr (!AHEAD) {
+        __syncwarp();
+        release(rg);
+        rg.advance();
+      }
     }
-    __syncwarp();
-    if (AHEAD && more) release(rk);
-    release(rv);
-    rk.advance();
-    rk.advance();
-    rv.advance();
-    rg.at = rv.at;  // where the next piece starts
-    rg.phase = rv.phase;
-    rv.advance();
     if constexpr (AHEAD) {
+      __syncwarp();
+      if (more) release(rk);
+      release(rv);
+      rk.advance();
+      rk.advance();
+      rv.advance();
+      rg.at = rv.at;  // where the next piece starts
+      rg.phase = rv.phase;
+      rv.advance();
 #pragma unroll
       for (int u = 0; u < U; ++u) {
 #pragma unroll
@@ -752,7 +788,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) decode_kv_kernel(const __grid_c
   // [page][head][K or V of 16 tokens]
   const uint32_t dbase = smem_u32(kvq_kv_dsmem), off = (1024u - (dbase & 1023u)) & 1023u;
   KvRing rg;
-  rg.stride = Gm::U * W * HB * Gm::HALF;
+  rg.stride = Gm::U * W * HB * Gm::ENTRY;
   rg.n = p.slots;
   rg.full = smem_u32(&s_full[0]);
   rg.empty = smem_u32(&s_empty[0]);
@@ -765,7 +801,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) decode_kv_kernel(const __grid_c
     const int UW = Gm::U * W;
     const int tpb = p.bs / kPage;  // tiles of a block
     const bool withhold = p.withhold >= 0 && report;
-    rg.addr = dbase + off + lane * HB * Gm::HALF;
+    rg.addr = dbase + off + lane * HB * Gm::ENTRY;
     rg.phase = 1;  // the slots start empty
     uint32_t issued = 0;
     bool more = next_piece(a, cur, pc);
@@ -783,7 +819,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) decode_kv_kernel(const __grid_c
         id[2] = id[3];
         id[3] = load_id(i + 4 * UW);
 #pragma unroll
-        for (int v = 0; v < 2; ++v) {
+        for (int v = 0; v < 2 * Gm::H; ++v) {  // K, then V, in H parts
           const uint32_t empty = rg.empty + 8 * rg.at, full = rg.full + 8 * rg.at;
           if (!__all_sync(FULL, mbar_test_wait(empty, rg.phase))) {  // until the workers release the slot, or one gave up
             const uint64_t start = global_ns();
@@ -798,10 +834,10 @@ __global__ void __launch_bounds__(kKvThreads, 1) decode_kv_kernel(const __grid_c
           if (!(withhold && rg.at == static_cast<uint32_t>(p.withhold))) {
             if (lane == 0) {
               if (v == 0) s_bad[rg.at] = bad;
-              mbar_arrive_expect_tx(full, min(UW, pc.n - i) * HB * Gm::HALF);
+              mbar_arrive_expect_tx(full, min(UW, pc.n - i) * HB * Gm::ENTRY);
             }
             __syncwarp();
-            if (mine) tma_load_5d(rg.addr + rg.at * rg.stride, v == 0 ? &p.k : &p.v, 0, row, 0, h0, blk, full);
+            if (mine) tma_load_5d(rg.addr + rg.at * rg.stride, v < Gm::H ? &p.k : &p.v, 0, row, v % Gm::H * (Gm::ROW / Gm::PB / Gm::H), h0, blk, full);
           }
           ++issued;
           rg.advance();
@@ -818,7 +854,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) decode_kv_kernel(const __grid_c
   // ---- worker: pages sub, sub + W, ... of each slot, kv head h, block cb of its query heads
   const int sub = warp / (HB * CB), hl = warp / CB % HB, cb = cg * CB + warp % CB;
   if (sub < W) {
-    const uint32_t mine = off + (sub * HB + hl) * Gm::HALF;
+    const uint32_t mine = off + (sub * HB + hl) * Gm::ENTRY;
     rg.addr = dbase + mine;
     bool ok = true;
     while (ok && next_piece(a, cur, pc)) {
@@ -983,12 +1019,12 @@ static kvq_status launch_kv(KvParams &p, int head_groups, const kvq_paged_kv *ca
   using Gm = KvGeom<D, CT, NT>;
   const int64_t es = CT == KV_E4M3 ? 1 : 2;
   const int HB = p.s.heads_per_cta;
-  if (!paged_tensor_map(cache->k, Gm::ROW, Gm::PB, HB, cache->k_stride_token * es, cache->k_stride_head * es,
+  if (!paged_tensor_map(cache->k, Gm::ROW, Gm::PB, Gm::ROW / Gm::PB / Gm::H, HB, cache->k_stride_token * es, cache->k_stride_head * es,
                         cache->k_stride_block * es, p.bs, p.s.Hk, cache->num_blocks, &p.k) ||
-      !paged_tensor_map(cache->v, Gm::ROW, Gm::PB, HB, cache->v_stride_token * es, cache->v_stride_head * es,
+      !paged_tensor_map(cache->v, Gm::ROW, Gm::PB, Gm::ROW / Gm::PB / Gm::H, HB, cache->v_stride_token * es, cache->v_stride_head * es,
                         cache->v_stride_block * es, p.bs, p.s.Hk, cache->num_blocks, &p.v))
     return KVQ_ERR_CUDA;
-  const int slot = Gm::U * p.s.warps_per_head * HB * Gm::HALF, parts = p.direct ? kKvWarps * 8 * NT * D * 4 : 0;
+  const int slot = Gm::U * p.s.warps_per_head * HB * Gm::ENTRY, parts = p.direct ? kKvWarps * 8 * NT * D * 4 : 0;
   const int fit = (Gm::RING - parts) / slot;
   p.slots = fit < kKvMaxSlots ? fit : kKvMaxSlots;
   const size_t smem = static_cast<size_t>(p.slots) * slot + parts + 1024;
@@ -1020,19 +1056,22 @@ static kvq_status launch_kv_type(KvParams &p, int groups, const kvq_paged_kv *ca
 template <int D>
 static kvq_status launch_kv_merge(const KvParams &p, cudaStream_t s) {
   const long long rows = static_cast<long long>(p.s.B) * p.s.Hq;
-  // partials of a row, on average: more than a warp reads in a round trip or two are shared by eight warps
+  // partials of a row, on average: more than a warp reads in a round trip or two are shared by four or eight warps
   const long long parts = static_cast<long long>(p.s.num_splits > 0 ? p.s.num_splits : p.s.seg_ctas / p.s.B + 1) * p.s.warps_per_head;
-  const bool many = parts > 16;
-  const long long ctas = many ? rows : (rows + 7) / 8;
+  constexpr int R = D < 256 ? 16 : 8;
+  const int wpr = parts <= R ? 1 : (parts <= 32 ? 4 : 8);
+  const long long ctas = (rows * wpr + 7) / 8;
   // 16 partials a round trip where one wave of CTAs has room for their registers (32 sequences x 32 heads: 95 us a call
   // against 97 with 8), else 8 (256 x 32: 95 us against 106 with 16)
-  const bool wide = D < 256 && ctas <= sm_count();
+  const bool wide = R > 8 && ctas <= sm_count();
   const dim3 grid(static_cast<unsigned>(ctas)), block(256);
   cudaError_t e;
-  if (many)
-    e = wide ? launch_dependent(kv_merge_kernel<D, 8, D < 256 ? 16 : 8>, grid, block, s, p.s) : launch_dependent(kv_merge_kernel<D, 8, 8>, grid, block, s, p.s);
+  if (wpr == 8)
+    e = launch_dependent(wide ? kv_merge_kernel<D, 8, R> : kv_merge_kernel<D, 8, 8>, grid, block, s, p.s);
+  else if (wpr == 4)
+    e = launch_dependent(wide ? kv_merge_kernel<D, 4, R> : kv_merge_kernel<D, 4, 8>, grid, block, s, p.s);
   else
-    e = wide ? launch_dependent(kv_merge_kernel<D, 1, D < 256 ? 16 : 8>, grid, block, s, p.s) : launch_dependent(kv_merge_kernel<D, 1, 8>, grid, block, s, p.s);
+    e = launch_dependent(wide ? kv_merge_kernel<D, 1, R> : kv_merge_kernel<D, 1, 8>, grid, block, s, p.s);
   return e == cudaSuccess ? launch_status() : KVQ_ERR_CUDA;
 }
 

@@ -84,10 +84,10 @@ bool int4_tensor_maps(const void *k_cache, const void *v_cache, const void *k_sc
 bool tq_tensor_map(const void *cache, long long num_blocks, int Hk, int slot_bytes, int row_bytes, CUtensorMap *map);
 
 // K or V of a kvq_paged_kv as {part_bytes, block_size, row_bytes / part_bytes, Hk, num_blocks} bytes, the parts of a
-// row apart; box {part_bytes, 16, all parts, box_heads, 1} = 16 rows of box_heads heads, stored [head][part][row][part_bytes]
+// row apart; box {part_bytes, 16, box_parts, box_heads, 1} = 16 rows of box_heads heads, stored [head][part][row][part_bytes]
 // with the 128B (part_bytes 128) or 64B swizzle. Strides in bytes, multiples of 16; encoded anew for each call (the caller's
 // addresses are not kept). False if the driver entry point is unavailable or the encode fails.
-bool paged_tensor_map(const void *base, int row_bytes, int part_bytes, int box_heads, long long token, long long head, long long block,
+bool paged_tensor_map(const void *base, int row_bytes, int part_bytes, int box_parts, int box_heads, long long token, long long head, long long block,
                       int block_size, int Hk, long long num_blocks, CUtensorMap *map);
 
 // Raise a kernel's dynamic shared-memory limit to `bytes` on the current device. The attribute
