@@ -189,13 +189,10 @@ __device__ __forceinline__ void store_out(const SplitArgs &a, long long row, int
   constexpr int V = D / 32;
   const long long e = row * D + lane * V;
   if (a.out_dtype == KVQ_F32) {
-    if constexpr (V % 4 == 0) {
-#pragma unroll
-      for (int j = 0; j < V; j += 4)
-        *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + e + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
-    } else {
+    if constexpr (V == 4)
+      *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + e) = make_float4(o[0], o[1], o[2], o[3]);
+    else
       *reinterpret_cast<float2 *>(static_cast<float *>(a.out) + e) = make_float2(o[0], o[1]);
-    }
   } else if (a.out_dtype == KVQ_BF16) {
 #pragma unroll
     for (int j = 0; j < V; j += 2)

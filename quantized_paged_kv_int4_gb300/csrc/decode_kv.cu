@@ -44,6 +44,7 @@
 
 #include "decode_common.cuh"
 #include "kvq_host.h"
+#include "kvq_step.cuh"
 
 namespace kvq {
 
@@ -142,6 +143,23 @@ __device__ __forceinline__ void mma_kv(float (&c)[4], uint32_t a0, uint32_t a1, 
 }
 __device__ __forceinline__ uint32_t bf2_as_u32(__nv_bfloat162 b) { return *reinterpret_cast<uint32_t *>(&b); }
 
+// The keys of sequence b that are read (as seq_span of decode_common.cuh), read through L2: the merge reads the lengths
+// ahead of its wait, where an L1 line could be from before the kernel that wrote them.
+__device__ __forceinline__ SeqSpan kv_span(const SplitArgs &a, int b, unsigned *flags) {
+  int L = __ldcg(a.seq_lens + b);
+  const int cap = a.max_blocks * kPage;
+  if (L > cap) {
+    if (flags != nullptr) atomicOr(flags, ERR_SEQLEN);
+    L = cap;
+  }
+  SeqSpan s;
+  s.L = max(L, 0);
+  s.lo = a.window > 0 ? max(0, s.L - a.window) : 0;
+  s.f = s.lo / kPage;
+  s.np = s.L > 0 ? (s.L - 1) / kPage - s.f + 1 : 0;
+  return s;
+}
+
 // The pieces of a CTA's run.
 struct KvPiece {
   int b, page, n, L, lo;  // pages page .. page + n - 1 of sequence b; live keys are [lo, L)
@@ -156,7 +174,7 @@ __device__ __forceinline__ bool next_piece(const SplitArgs &a, KvCursor &c, KvPi
     const int b = c.b, s = static_cast<int>(blockIdx.x) % a.num_splits;
     if (b < 0) return false;
     c.b = -1;
-    const SeqSpan sp = seq_span(a, b, nullptr);
+    const SeqSpan sp = kv_span(a, b, nullptr);
     const int per = (sp.np + a.num_splits - 1) / a.num_splits;
     const long long lo = static_cast<long long>(s) * per, left = sp.np - lo;
     pc = {b, sp.f + static_cast<int>(lo), static_cast<int>(min(static_cast<long long>(per), left)), sp.L, sp.lo,
@@ -165,7 +183,7 @@ __device__ __forceinline__ bool next_piece(const SplitArgs &a, KvCursor &c, KvPi
   }
   while (c.P < c.pe && c.b < a.B) {
     const int b = c.b++;
-    const SeqSpan sp = seq_span(a, b, nullptr);
+    const SeqSpan sp = kv_span(a, b, nullptr);
     const long long P = c.P;
     c.P += sp.np;
     if (sp.np > 0) {
@@ -213,7 +231,7 @@ __device__ __forceinline__ bool kv_piece(const KvParams &p, KvRing &rg, uint8_t 
   uint32_t qf[NT][MT][2];
   float sc[NT][2];   // score scale of columns 2t, 2t + 1
   float slope[NT][2];
-  const float k_scale = CT == KV_E4M3 && p.k_scale != nullptr ? __ldg(p.k_scale + h) : 1.f;
+  const float k_scale = CT == KV_E4M3 && p.k_scale != nullptr ? p.k_scale[h] : 1.f;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const int col = FOLD ? (g & 3) : c0 + 8 * nt + g;
@@ -223,8 +241,8 @@ __device__ __forceinline__ bool kv_piece(const KvParams &p, KvRing &rg, uint8_t 
     if constexpr (CT != KV_E4M3) {
 #pragma unroll
       for (int ks = 0; ks < MT; ++ks) {
-        qf[nt][ks][0] = live ? __ldg(qr + 8 * ks + t) : 0u;
-        qf[nt][ks][1] = live ? __ldg(qr + 8 * ks + 4 + t) : 0u;
+        qf[nt][ks][0] = live ? qr[8 * ks + t] : 0u;
+        qf[nt][ks][1] = live ? qr[8 * ks + 4 + t] : 0u;
       }
       sc[nt][0] = sc[nt][1] = p.sc_log2;
     } else {
@@ -235,7 +253,7 @@ __device__ __forceinline__ bool kv_piece(const KvParams &p, KvRing &rg, uint8_t 
       };
 #pragma unroll
       for (int ks = 0; ks < MT; ++ks) {
-        const uint2 r = live ? __ldg(reinterpret_cast<const uint2 *>(qr + 8 * ks + 2 * t)) : make_uint2(0u, 0u);
+        const uint2 r = live ? *reinterpret_cast<const uint2 *>(qr + 8 * ks + 2 * t) : make_uint2(0u, 0u);
         qf[nt][ks][0] = r.x;
         qf[nt][ks][1] = r.y;
       }
@@ -266,7 +284,7 @@ __device__ __forceinline__ bool kv_piece(const KvParams &p, KvRing &rg, uint8_t 
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int cc = FOLD ? ((2 * t + i) & 3) : c0 + 8 * nt + 2 * t + i;
-        slope[nt][i] = p.alibi != nullptr && cc < G ? __ldg(p.alibi + h * G + cc) * 1.4426950408889634f : 0.f;
+        slope[nt][i] = p.alibi != nullptr && cc < G ? p.alibi[h * G + cc] * 1.4426950408889634f : 0.f;
       }
     }
   }
@@ -336,8 +354,8 @@ __device__ __forceinline__ bool kv_piece(const KvParams &p, KvRing &rg, uint8_t 
         out[nt][e] = NC == 4 ? (S.c[0][nt][e] + S.c[1][nt][e]) + (S.c[2][nt][e] + S.c[NC - 1][nt][e]) : S.c[0][nt][e] + S.c[1][nt][e];
     }
   };
-  // Ring entries come K, V, K, V, ... (H = 2: two of K, two of V): a step takes U tiles from each. AHEAD: K of the next step together with V of
-  // this one, so that the next scores are on the tensor cores while this step's weights are computed.
+  // Ring entries come K, V, K, V, ... (H = 2: two of K, two of V): a step takes U tiles from each. AHEAD: K of the next
+  // step together with V of this one, so that the next scores are on the tensor cores while this step's weights are computed.
   KvRing rk = rg, rv = rg;  // AHEAD: the next K and V; else rg is the one place
   rv.advance();
   const int per = U * W, steps = (pc.n + per - 1) / per;
@@ -589,7 +607,7 @@ __device__ __forceinline__ bool kv_piece(const KvParams &p, KvRing &rg, uint8_t 
 
   // ---- the piece's partial: lane (g, t) has columns 2t, 2t + 1 at two dims of each m-tile, 16 k + g and + 8 (FP8:
   // 16 k + 2g and + 1)
-  const float v_scale = CT == KV_E4M3 && p.v_scale != nullptr ? __ldg(p.v_scale + h) : 1.f;
+  const float v_scale = CT == KV_E4M3 && p.v_scale != nullptr ? p.v_scale[h] : 1.f;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -677,6 +695,28 @@ __device__ __forceinline__ void kv_join(const SplitArgs &a, int hq, long long n_
   }
 }
 
+// A lane's D / 32 consecutive elements of an output row.
+template <int D>
+__device__ __forceinline__ void kv_store(const SplitArgs &a, long long row, int lane, const float (&o)[D / 32]) {
+  if constexpr (D < 256) {
+    store_out<D>(a, row, lane, o);
+  } else {
+    const long long e = row * D + lane * 8;
+    if (a.out_dtype == KVQ_F32) {
+      float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + e);
+      dst[0] = make_float4(o[0], o[1], o[2], o[3]);
+      dst[1] = make_float4(o[4], o[5], o[6], o[7]);
+    } else {
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        w[j] = a.out_dtype == KVQ_BF16 ? bf2_as_u32(__floats2bfloat162_rn(o[2 * j], o[2 * j + 1]))
+                                       : h2_as_u32(__floats2half2_rn(o[2 * j], o[2 * j + 1]));
+      *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + e) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+}
+
 // The finished row (b, hq): the sink joins the denominator, then o / den, and the log-sum-exp on request. A row without
 // keys is zero (lse: the sink alone, or -inf); a NaN among the scores makes row and lse NaN.
 template <int D>
@@ -696,10 +736,10 @@ __device__ __forceinline__ void kv_finish(const SplitArgs &a, int b, int hq, int
   for (int j = 0; j < V; ++j) o[j] *= inv;
   const long long row = static_cast<long long>(b) * a.Hq + hq;
   if (a.lse_out != nullptr && lane == 0) a.lse_out[row] = den != 0.f ? (M + log2f(den)) * 0.6931471805599453f : -INFINITY;
-  store_out<D>(a, row, lane, o);
+  kv_store<D>(a, row, lane, o);
 }
 __device__ __forceinline__ float kv_sink2(const SplitArgs &a, int hq) {
-  return a.sinks != nullptr ? __ldg(a.sinks + hq) * 1.4426950408889634f : -INFINITY;
+  return a.sinks != nullptr ? __ldcg(a.sinks + hq) * 1.4426950408889634f : -INFINITY;
 }
 
 // Inclusive sum over the first 256 threads (all threads of the block call it); the total to *total.
@@ -723,6 +763,7 @@ __device__ __forceinline__ long long kv_scan(long long v, long long *scratch, lo
   *total = all;
   return v + before;
 }
+
 extern __shared__ __align__(1024) uint8_t kvq_kv_dsmem[];
 
 template <int D, int CT, int NT, bool FOLD, bool MODS>
@@ -755,12 +796,12 @@ __global__ void __launch_bounds__(kKvThreads, 1) decode_kv_kernel(const __grid_c
   if (a.num_splits > 0) {
     cur.b = blockIdx.x / a.num_splits;
     if (report)
-      for (int b = tid; b < a.B; b += kKvThreads) clamped_len(a, b, &g_flags_decode_kv);
+      for (int b = tid; b < a.B; b += kKvThreads) kv_span(a, b, &g_flags_decode_kv);
   } else {
     long long pages = 0, chunk = 0, np = 0, incl = 0;
     for (int base = 0; base < a.B; base += 256) {
       const int b = base + tid;
-      np = tid < 256 && b < a.B ? seq_span(a, b, report ? &g_flags_decode_kv : nullptr).np : 0;
+      np = tid < 256 && b < a.B ? kv_span(a, b, report ? &g_flags_decode_kv : nullptr).np : 0;
       incl = kv_scan(np, s_scan, &chunk);
       pages += chunk;
     }
@@ -771,7 +812,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) decode_kv_kernel(const __grid_c
     for (int base = 0; base < a.B; base += 256) {
       const int b = base + tid;
       if (a.B > 256) {
-        np = tid < 256 && b < a.B ? seq_span(a, b, nullptr).np : 0;
+        np = tid < 256 && b < a.B ? kv_span(a, b, nullptr).np : 0;
         incl = kv_scan(np, s_scan, &chunk) + before;
         before += chunk;
       }
@@ -807,7 +848,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) decode_kv_kernel(const __grid_c
     bool more = next_piece(a, cur, pc);
     while (more) {
       const int32_t *bt = p.block_table + static_cast<long long>(pc.b) * p.bt_stride;
-      auto load_id = [&](int i) { return lane < UW && i + lane < pc.n ? __ldg(bt + (pc.page + i + lane) / tpb) : 0; };
+      auto load_id = [&](int i) { return lane < UW && i + lane < pc.n ? bt[(pc.page + i + lane) / tpb] : 0; };
       int id[4] = {load_id(0), load_id(UW), load_id(2 * UW), load_id(3 * UW)};  // the next slots' blocks, ahead of their use
       for (int i = 0; i < pc.n && more; i += UW) {
         const bool mine = lane < UW && i + lane < pc.n, ok = id[0] >= 0 && id[0] < p.num_blocks;
@@ -837,7 +878,9 @@ __global__ void __launch_bounds__(kKvThreads, 1) decode_kv_kernel(const __grid_c
               mbar_arrive_expect_tx(full, min(UW, pc.n - i) * HB * Gm::ENTRY);
             }
             __syncwarp();
-            if (mine) tma_load_5d(rg.addr + rg.at * rg.stride, v < Gm::H ? &p.k : &p.v, 0, row, v % Gm::H * (Gm::ROW / Gm::PB / Gm::H), h0, blk, full);
+            if (mine)
+              tma_load_5d(rg.addr + rg.at * rg.stride, v < Gm::H ? &p.k : &p.v, 0, row, v % Gm::H * (Gm::ROW / Gm::PB / Gm::H),
+                          h0, blk, full);
           }
           ++issued;
           rg.advance();
@@ -863,7 +906,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) decode_kv_kernel(const __grid_c
                                            p.direct ? s_part + warp * 8 * NT * D : a.part_o + row * D,
                                            p.direct ? &s_lse[warp][0] : a.part_lse + row);
       if (a.num_splits == 0 && tid == 0 && blockIdx.y == 0) {  // the sequence's first and last CTA, for the merge
-        const SeqSpan sp = seq_span(a, pc.b, nullptr);
+        const SeqSpan sp = kv_span(a, pc.b, nullptr);
         if (pc.page == sp.f) a.seg_first[pc.b] = static_cast<int>(blockIdx.x);
         if (pc.page + pc.n == sp.f + sp.np) a.seg_last[pc.b] = static_cast<int>(blockIdx.x);
       }
@@ -874,7 +917,7 @@ __global__ void __launch_bounds__(kKvThreads, 1) decode_kv_kernel(const __grid_c
     asm volatile("bar.sync 1, 256;" ::: "memory");
     constexpr int V = D / 32, COLS = 8 * NT;
     const int b = blockIdx.x;
-    const bool empty = seq_span(a, b, nullptr).np == 0;
+    const bool empty = kv_span(a, b, nullptr).np == 0;
     for (int i = warp; i < HB * CB * COLS; i += kKvWarps) {
       const int group = i / COLS, col = (cg * CB + group % CB) * COLS + i % COLS, hq = (h0 + group / CB) * a.G + col;
       if (col >= a.G) continue;
@@ -906,12 +949,12 @@ __global__ void __launch_bounds__(256) kv_merge_kernel(const SplitArgs a) {
   const long long idx = static_cast<long long>(blockIdx.x) * (8 / WPR) + warp / WPR;
   const bool live = idx < static_cast<long long>(a.B) * a.Hq;
   const int b = live ? static_cast<int>(idx / a.Hq) : 0, hq = live ? static_cast<int>(idx % a.Hq) : 0;
-  const SeqSpan sp = live ? seq_span(a, b, nullptr) : SeqSpan{0, 0, 0, 0};
+  const SeqSpan sp = live ? kv_span(a, b, nullptr) : SeqSpan{0, 0, 0, 0};
   const float sink2 = kv_sink2(a, hq);
   long long lo = 0, hi = 0;
   const bool scan = a.num_splits == 0 && a.B <= 256;  // uniform
   if (scan) {
-    const long long np = tid < a.B ? seq_span(a, tid, nullptr).np : 0;
+    const long long np = tid < a.B ? kv_span(a, tid, nullptr).np : 0;
     long long pages;
     s_page[tid] = kv_scan(np, s_scan, &pages) - np;
     __syncthreads();

@@ -16,7 +16,7 @@ constexpr unsigned FULL = 0xffffffffu;
 constexpr int kPage = 16;  // tokens per page: one MMA M-tile of the read kernels
 
 // Device-side error flags (kvq_device_error).
-enum : unsigned { ERR_BLOCK = 1u, ERR_SEQLEN = 2u, ERR_SLOT = 4u, ERR_TIMEOUT = 8u, ERR_RANGE = 16u, ERR_FREE = 32u };
+enum : unsigned { ERR_BLOCK = 1u, ERR_SEQLEN = 2u, ERR_SLOT = 4u, ERR_TIMEOUT = 8u, ERR_RANGE = 16u };
 
 // 2^k for an integer k in [-126, 127], exact.
 __device__ __forceinline__ float pow2i(int k) { return __int_as_float((k + 127) << 23); }
@@ -174,15 +174,6 @@ __device__ __forceinline__ float fast_exp2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
-}
-
-// Start of a kernel that may be launched as a programmatic dependent of the one before it on its stream (any kernel):
-// wait until that one has finished and its writes are visible, then let the next launch begin -- in this order, so that
-// whatever the next kernel reads ahead of its own wait was finished before this kernel. Every CTA calls it: a grid that
-// could end without waiting would release its successor while its predecessor still runs.
-__device__ __forceinline__ void pdl_enter() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // ---------------------------------------------------------------------------------------------

@@ -13,8 +13,8 @@
 // reads it and one changes it. A call whose entries and tokens fit one CTA's few rounds does it behind
 // a barrier; a larger one leaves it to a second, one-CTA kernel.
 
-#include "kvq_device.cuh"
 #include "kvq_host.h"
+#include "kvq_step.cuh"
 
 namespace kvq {
 
@@ -48,8 +48,8 @@ struct Request {
 __device__ __forceinline__ Request load_request(const PlanArgs &a, int b, unsigned *flags) {
   Request r;
   const long long cap = static_cast<long long>(a.max_blocks) * a.bs;
-  const long long c = __ldg(a.context + b), q = a.query != nullptr ? __ldg(a.query + b) : 1;
-  r.row = a.rows != nullptr ? __ldg(a.rows + b) : b;
+  const long long c = a.context[b], q = a.query != nullptr ? a.query[b] : 1;
+  r.row = a.rows != nullptr ? a.rows[b] : b;
   r.n = q < 0 ? 0 : q;
   r.ctx = c < 0 ? 0 : (c > cap ? cap : c);
   const long long L = (c < 0 ? 0 : c) + r.n;
@@ -74,7 +74,7 @@ __device__ __forceinline__ int block_id(const PlanArgs &a, const Request &r, int
     atomicOr(flags, ERR_FREE);
     return -1;
   }
-  const int id = __ldg(a.free_blocks + i);
+  const int id = a.free_blocks[i];
   if (id < 0 || id >= a.num_blocks) {
     atomicOr(flags, ERR_BLOCK);
     return -1;

@@ -23,8 +23,8 @@
 
 #include <type_traits>
 
-#include "kvq_device.cuh"
 #include "kvq_host.h"
+#include "kvq_step.cuh"
 
 namespace kvq {
 
@@ -69,7 +69,7 @@ __device__ __forceinline__ uint8_t to_fp8(float x, float inv) {
   return static_cast<uint8_t>(__nv_cvt_float_to_fp8(x * inv, __NV_SATFINITE, __NV_E4M3));
 }
 __device__ __forceinline__ float fp8_inv(const float *scales, int head) {
-  return scales != nullptr ? __frcp_rn(__ldg(scales + head)) : 1.f;
+  return scales != nullptr ? __frcp_rn(scales[head]) : 1.f;
 }
 template <int T>
 __device__ __forceinline__ void store1(void *p, long long i, float x, float inv) {
@@ -145,7 +145,7 @@ __device__ __forceinline__ void store8(void *p, long long i, const float (&x)[8]
 // cos and sin of the token's pairs, times the factor, into the warp's shared memory
 __device__ __forceinline__ void fill_angles(const WriteKvParams &p, int pos, int lane, float2 *cs) {
   for (int i = lane; i < p.half; i += 32) {
-    const uint64_t turn = static_cast<uint64_t>(static_cast<uint32_t>(pos)) * __ldg(p.freqs + i);  // mod 2^64: mod a turn
+    const uint64_t turn = static_cast<uint64_t>(static_cast<uint32_t>(pos)) * p.freqs[i];  // mod 2^64: mod a turn
     const float x = static_cast<float>(static_cast<int32_t>(turn >> 32)) * 4.656612873077393e-10f;  // 2^-31: units of pi
     float s, c;
     sincospif(x, &s, &c);
@@ -241,12 +241,12 @@ __global__ void __launch_bounds__(32 * kWriteWarps) write_kv_kernel(const WriteK
   pl.a = pl.turns ? j : rc + j - ri;
   pl.b = pl.turns ? (j + ri < rc ? j + ri : -1) : (j - ri + pi < pc ? rc + j - ri + pi : -1);
   const Place pv = {j, j + vi < vc ? j + vi : -1, j < vi, false};
-  const int pos = rot ? __ldg(p.positions + t) : 0;
+  const int pos = rot ? p.positions[t] : 0;
   if (pos < 0) return;  // padding
   bool kv = true;
   long long kd = 0, vd = 0;  // element offsets of the token in the pools
   if constexpr (POOL >= 0) {
-    const long long slot = __ldg(p.slots + t);
+    const long long slot = p.slots[t];
     kv = slot >= 0 && slot < p.num_blocks * p.bs;
     if (slot >= 0 && !kv && part == 0 && lane == 0) atomicOr(&g_flags_write_kv, ERR_SLOT);
     if (kv) {

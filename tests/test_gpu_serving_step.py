@@ -104,17 +104,24 @@ def test_rotary_and_plan_before_the_int4_cache():
     assert (np.abs(f64(out) - ref) <= 2e-3 + 1e-2 * np.abs(ref)).all()
 
 
-def test_captured_serving_step():
-    """Plan, write and decode in one graph, replayed over many steps, against the same steps run eagerly."""
-    Hq, Hk, D, bs, nb, B, steps = 8, 2, 128, 16, 40, 3, 40
+@pytest.mark.parametrize("start", [0, 700])
+def test_captured_serving_step(start):
+    """Plan, write and decode in one graph, replayed over many steps, against the same steps run eagerly: short tables
+    (one decode launch) and long ones (split and join, whose second kernel reads the lengths early)."""
+    Hq, Hk, D, bs, B, steps = 8, 2, 128, 16, 3, 40
+    held = -(-start // bs)  # blocks that the requests hold at the start
+    width, nb = held + 8 if start == 0 else 64, B * (held + 4) + 4
     dev = dict(device="cuda")
     freqs, _ = kvq.kvq_rope_frequencies(D, 10000.0, device="cuda")
     xs = torch.randn((steps, B, Hq + 2 * Hk, D), generator=torch.Generator().manual_seed(3)).to(BF).cuda()
 
     def fresh():
-        return dict(kc=torch.zeros((nb, bs, Hk, D), dtype=BF, **dev), vc=torch.zeros((nb, bs, Hk, D), dtype=BF, **dev),
-                    table=torch.full((B, 8), -1, dtype=torch.int32, **dev), cursor=torch.zeros(1, dtype=torch.int64, **dev),
-                    free=torch.arange(nb, dtype=torch.int32, **dev), context=torch.zeros(B, dtype=torch.int32, **dev),
+        g = torch.Generator().manual_seed(4)
+        table = torch.full((B, width), -1, dtype=torch.int32)
+        table[:, :held] = torch.arange(B * held).view(B, held)
+        return dict(kc=torch.randn((nb, bs, Hk, D), generator=g).to(BF).cuda(), vc=torch.randn((nb, bs, Hk, D), generator=g).to(BF).cuda(),
+                    table=table.cuda(), cursor=torch.tensor([B * held], **dev),
+                    free=torch.arange(nb, dtype=torch.int32, **dev), context=torch.full((B,), start, dtype=torch.int32, **dev),
                     x=xs[0].clone(), out=torch.empty((B, Hq, D), dtype=BF, **dev), lens=torch.empty(B, dtype=torch.int32, **dev),
                     pos=torch.empty(B, dtype=torch.int32, **dev), slots=torch.empty(B, dtype=torch.int64, **dev),
                     q=torch.empty((B, Hq, D), dtype=BF, **dev),
@@ -141,4 +148,6 @@ def test_captured_serving_step():
             run()
         torch.cuda.synchronize()
         assert torch.equal(a["out"], b["out"]) and torch.equal(a["table"], b["table"]), i
-    assert int(a["context"][0]) == steps and torch.equal(a["kc"], b["kc"]) and kvq.kvq_device_error() == (0, 0)
+        ref, _, size = paged_kv.decode(f64(a["q"]), f64(a["kc"]), f64(a["vc"]), a["table"].cpu().numpy(), a["lens"].tolist(), D ** -0.5)
+        assert (np.abs(f64(a["out"]) - ref) <= 2.0 ** -11 * size + 2.0 ** -8 * np.abs(ref) * 1.01 + 1e-7).all(), i
+    assert int(a["context"][0]) == start + steps and torch.equal(a["kc"], b["kc"]) and kvq.kvq_device_error() == (0, 0)
