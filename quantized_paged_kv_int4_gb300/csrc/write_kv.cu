@@ -456,10 +456,10 @@ extern "C" kvq_status kvq_write_kv(const void *key, int64_t k_stride_t, int64_t 
   if (D % 8 != 0 || D > 256 || static_cast<long long>(Hq) + Hk > 65536) return KVQ_ERR_UNSUPPORTED;
   const kvq_status sc = check_paged_kv(cache, dtype);
   if (sc != KVQ_OK) return sc;
-  if ((Hq > 0) != (q != nullptr) || (Hq > 0) != (q_out != nullptr) || (Hq > 0 && rotary == nullptr))
-    return KVQ_ERR_INVALID_ARG;
-  WriteKvParams p = {};
+  if (Hq > 0 && rotary == nullptr) return KVQ_ERR_INVALID_ARG;
   if (T == 0) return KVQ_OK;
+  if ((Hq > 0) != (q != nullptr) || (Hq > 0) != (q_out != nullptr)) return KVQ_ERR_INVALID_ARG;
+  WriteKvParams p = {};
   const kvq_status st = check_rotary(rotary, D, &p);
   if (st != KVQ_OK) return st;
   if (!key || !value || !slot_mapping || !aligned(slot_mapping, 8)) return KVQ_ERR_INVALID_ARG;

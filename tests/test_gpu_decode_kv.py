@@ -299,6 +299,22 @@ def test_repeatable_and_on_another_stream_and_captured():
     c.check()
 
 
+def test_no_sequences_and_captured_without_a_workspace():
+    c = Case([700, 33], 8, 2, 128, BF, seed=16)
+    q, table, lens = c.q.cuda(), c.table.cuda(), c.lens.cuda()
+    none = kvq.kvq_decode_kv(q[:0], c.k, c.v, table[:0], lens[:0], c.scale)
+    assert none.shape == (0, 8, 128)
+    want = c.run()[0]
+    out, stream = torch.empty_like(q), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    step = kvq.CapturedStep(lambda: kvq.kvq_decode_kv(q, c.k, c.v, table, lens, c.scale, out=out), stream)
+    out.zero_()
+    torch.cuda.synchronize()
+    step()
+    stream.synchronize()
+    assert torch.equal(out, want) and kvq.kvq_device_error() == (0, 0)
+
+
 def test_calls_at_once_on_two_streams():
     """Two batches on two streams, several times, each with a workspace of its own: the bits of the calls alone."""
     cases = [Case([3000, 77, 1024], 8, 2, 128, BF, seed=21), Case([900, 4000], 16, 8, 64, E4, seed=22)]

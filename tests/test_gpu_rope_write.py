@@ -182,6 +182,17 @@ def test_write_without_rotation_is_a_copy():
         assert torch.equal(c.flatten(0, 1)[slots[keep]], x[keep])
 
 
+def test_no_tokens():
+    x = torch.zeros((0, 4, 64), dtype=BF, device="cuda")
+    pos, slots = torch.zeros(0, dtype=torch.int32).cuda(), torch.zeros(0, dtype=torch.int64).cuda()
+    freqs, _ = freqs_of(64)
+    kc, vc = pool_of(2, 16, 4, 64, "apart", BF)
+    assert kvq.kvq_write_kv(x, x, kc, vc, slots, q=x, positions=pos, freqs=freqs).shape == x.shape
+    assert kvq.kvq_write_kv(x, x, kc, vc, slots) is None
+    q, k = kvq.kvq_rope(x, x, pos, freqs)
+    assert q.shape == k.shape == x.shape and (kc == 3).all() and (vc == 3).all()
+
+
 def test_fp8_write_saturates_and_keeps_nan():
     x = torch.tensor([1e30, -1e30, float("inf"), float("-inf"), float("nan"), 447.9, 464.0, 2.0 ** -10]).repeat(2)[None, None]
     kc, vc = pool_of(1, 16, 1, 16, "apart", E4)
