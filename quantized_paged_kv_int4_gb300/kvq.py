@@ -516,6 +516,7 @@ def kvq_device_error(stream=None):
 # ----------------------------------------------------------------------------------------------
 # These calls are small and frequent (a step of 32 tokens), so their arguments are checked and passed by a native module
 # (native/binding.cpp) instead of ctypes: about 1 us a call instead of 6 to 10.
+# stream=s is the call under torch.cuda.stream(s): outputs that are not given, and decode's workspace, are memory of s.
 _native_module = None
 
 

@@ -95,20 +95,32 @@ bool truth(PyObject *o) {
   return v != 0;
 }
 
-// The call's stream and, while it lives, its device as the current one.
+int64_t attribute(PyObject *o, const char *name) {
+  PyObject *v = PyObject_GetAttrString(o, name);
+  if (v == nullptr) throw PyError{};
+  const long long r = PyLong_AsLongLong(v);
+  Py_DECREF(v);
+  if (r == -1 && PyErr_Occurred()) throw PyError{};
+  return r;
+}
+
+// The call's stream and, while it lives, its device and (when given) its stream as the current ones: memory for outputs
+// and workspaces has to come from the stream that uses it, as another's may still be in use there.
 struct Place {
   c10::cuda::OptionalCUDAGuard guard;
+  c10::cuda::OptionalCUDAStreamGuard on_stream;
   kvq_stream_t stream;
   Place(PyObject *o, int dev) {
     if (c10::cuda::current_device() != dev) guard.set_index(static_cast<c10::DeviceIndex>(dev));
     if (o == Py_None) {
       stream = c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream();
     } else {
-      PyObject *raw = PyObject_GetAttrString(o, "cuda_stream");
-      if (raw == nullptr) throw PyError{};
-      stream = reinterpret_cast<kvq_stream_t>(PyLong_AsUnsignedLongLong(raw));
-      Py_DECREF(raw);
-      if (PyErr_Occurred()) throw PyError{};
+      const int64_t at = attribute(o, "device_index");
+      if (at != dev) fail(PyExc_ValueError, "the stream is on cuda:%d, the call on cuda:%d", static_cast<int>(at), dev);
+      const c10::cuda::CUDAStream s = c10::cuda::CUDAStream::unpack3(attribute(o, "stream_id"), static_cast<c10::DeviceIndex>(at),
+                                                                     c10::DeviceType::CUDA);
+      on_stream.reset_stream(s);
+      stream = s.stream();
     }
   }
 };
@@ -229,6 +241,7 @@ PyObject *plan_step(PyObject *const *a) {
     T = cuda_tensor(given, "positions / slot_mapping").numel();
   }
   Made out[4];
+  const Place place(a[15], dev);
   const int64_t sizes[4] = {B, B + 1, T, T};
   const char *names[4] = {"seq_lens", "query_start_loc", "positions", "slot_mapping"};
   void *p[4];
@@ -247,7 +260,6 @@ PyObject *plan_step(PyObject *const *a) {
   const void *query = sized_or_null(a[1], "query_lens", at::kInt, dev, B), *rows = sized_or_null(a[7], "rows", at::kInt, dev, B);
   const void *cursor = sized_or_null(a[4], "cursor", at::kLong, dev, 1);
   void *cursor_out = a[9] == Py_None ? const_cast<void *>(cursor) : sized(a[9], "cursor_out", at::kLong, dev, 1);
-  const Place place(a[15], dev);
   check(kvq_plan_step(static_cast<const int32_t *>(context.data_ptr()), static_cast<const int32_t *>(query),
                       static_cast<const int32_t *>(rows), static_cast<int32_t *>(table.data_ptr()), count32(width, "max_blocks"),
                       table.size(0), static_cast<const int32_t *>(free_blocks), num_free, static_cast<const int64_t *>(cursor),
@@ -288,11 +300,11 @@ PyObject *rope(PyObject *const *a) {
   if (x.dim() != 3) fail(PyExc_ValueError, "q / k must be [T, heads, D]");
   const int64_t T = x.size(0), D = x.size(2);
   if ((a[0] == Py_None && a[6] != Py_None) || (a[1] == Py_None && a[7] != Py_None)) fail(PyExc_ValueError, "an output without its input");
+  const Place place(a[8], dev);
   Rotated q, k;
   if (a[0] != Py_None) q.set(a[0], a[6], "q", "q_out", type, dev, T, D);
   if (a[1] != Py_None) k.set(a[1], a[7], "k", "k_out", type, dev, T, D);
   const kvq_rotary r = rotary_of(a[2], a[3], a[4], a[5], T, D, dev);
-  const Place place(a[8], dev);
   check(kvq_rope(q.in.p, q.in.st, q.in.sh, q.out.p, q.out.st, q.out.sh, count32(q.in.heads, "heads"), k.in.p, k.in.st, k.in.sh,
                  k.out.p, k.out.st, k.out.sh, count32(k.in.heads, "heads"), &r, row_code(type), count32(T, "T"), count32(D, "D"),
                  place.stream),
@@ -320,6 +332,7 @@ PyObject *write_kv(PyObject *const *a) {
   if ((a[8] == Py_None) != (a[9] == Py_None)) fail(PyExc_ValueError, "positions and freqs go together");
   kvq_rotary r;
   const bool rot = a[8] != Py_None;
+  const Place place(a[13], dev);
   if (rot) r = rotary_of(a[8], a[9], a[10], a[11], T, D, dev);
   Rotated q;
   if (a[7] != Py_None) {
@@ -328,7 +341,6 @@ PyObject *write_kv(PyObject *const *a) {
   } else if (a[12] != Py_None) {
     fail(PyExc_ValueError, "q_out without q");
   }
-  const Place place(a[13], dev);
   check(kvq_write_kv(k.p, k.st, k.sh, v.p, v.st, v.sh, &cache, static_cast<const int64_t *>(slots), q.in.p, q.in.st, q.in.sh, q.out.p,
                      q.out.st, q.out.sh, count32(q.in.heads, "heads"), rot ? &r : nullptr, row_code(type), count32(T, "T"),
                      count32(k.heads, "heads"), count32(D, "D"), place.stream),
@@ -352,6 +364,7 @@ PyObject *decode_kv(PyObject *const *a) {
   if (table.dim() != 2 || table.size(0) != B) fail(PyExc_ValueError, "block_table must be [B, max_blocks] with B = %d", B);
   const void *lens = sized(a[4], "seq_lens", at::kInt, dev, B);
   Made out, ws;
+  const Place place(a[12], dev);
   PyObject *o = a[8];
   if (o != Py_None) {
     out.take(o);
@@ -380,16 +393,10 @@ PyObject *decode_kv(PyObject *const *a) {
     if (l.dim() != 2 || l.size(0) != B || l.size(1) != Hq) fail(PyExc_ValueError, "lse_out must be [%d, %d]", B, Hq);
     mods.lse_out = static_cast<float *>(l.data_ptr());
   }
-  const Place place(a[12], dev);
   PyObject *w = a[9];
   if (w == Py_None) {
     const int64_t need = static_cast<int64_t>(kvq_decode_kv_workspace_bytes(B, Hq, Hk, D, splits));
     w = ws.make({need > 16 ? need : 16}, at::kByte, q);
-    if (a[12] != Py_None) {  // freed when this call returns, in use on its stream until the kernels end
-      PyObject *r = PyObject_CallMethod(w, "record_stream", "O", a[12]);
-      if (r == nullptr) throw PyError{};
-      Py_DECREF(r);
-    }
   }
   const at::Tensor &work = on(w, "workspace", at::kByte, dev);
   check(kvq_decode_kv(q.data_ptr(), row_code(type), &cache, static_cast<const int32_t *>(table.data_ptr()),

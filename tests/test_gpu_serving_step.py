@@ -151,3 +151,31 @@ def test_captured_serving_step(start):
         ref, _, size = paged_kv.decode(f64(a["q"]), f64(a["kc"]), f64(a["vc"]), a["table"].cpu().numpy(), a["lens"].tolist(), D ** -0.5)
         assert (np.abs(f64(a["out"]) - ref) <= 2.0 ** -11 * size + 2.0 ** -8 * np.abs(ref) * 1.01 + 1e-7).all(), i
     assert int(a["context"][0]) == start + steps and torch.equal(a["kc"], b["kc"]) and kvq.kvq_device_error() == (0, 0)
+
+
+def test_new_outputs_belong_to_the_stream_that_writes_them():
+    """A block that the current stream has freed but not yet finished with must not become the output of a call on
+    another stream: the fill that is still pending would land in it."""
+    x = torch.randn((64, 8, 128), generator=torch.Generator().manual_seed(31)).bfloat16().cuda()
+    pos = torch.arange(64, dtype=torch.int32, device="cuda")
+    freqs, _ = kvq.kvq_rope_frequencies(128, device="cuda")
+    lens = torch.full((64,), 5, dtype=torch.int32, device="cuda")
+    table = torch.zeros((64, 1), dtype=torch.int32, device="cuda")
+    pools = [torch.randn((1, 16, 2, 128), generator=torch.Generator().manual_seed(32 + i)).bfloat16().cuda() for i in range(2)]
+    slots = torch.full((64,), -1, dtype=torch.int64, device="cuda")
+    calls = (lambda s: kvq.kvq_rope(x, None, pos, freqs, stream=s)[0],
+             lambda s: kvq.kvq_write_kv(x[:, :2], x[:, 2:4], *pools, slots, q=x, positions=pos, freqs=freqs, stream=s),
+             lambda s: kvq.kvq_decode_kv(x, *pools, table, lens, 0.1, stream=s),
+             lambda s: kvq.kvq_decode_kv(x, *pools, table, lens, 0.1, num_splits=1, out_dtype=torch.float32, stream=s),
+             lambda s: kvq.kvq_plan_step(lens, None, table, None, None, 16, 1, T=64, stream=s)[3])
+    for call in calls:
+        want, side = call(None).clone(), torch.cuda.Stream()
+        torch.cuda.synchronize()
+        pending = torch.empty_like(want)
+        torch.cuda._sleep(20_000_000)  # about 10 ms
+        pending.fill_(7)
+        del pending
+        out = call(side)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    assert kvq.kvq_device_error() == (0, 0)
