@@ -484,7 +484,7 @@ KVQ_API kvq_status kvq_rope_frequencies(int32_t rotary_dim, double base, const k
  *   q, k          [T, Hq, D] and [T, Hk, D] of dtype (KVQ_BF16 / KVQ_F16 / KVQ_F32); element (t, h, d) at
  *                 ptr + t*stride_t + h*stride_h + d. q may be NULL with Hq == 0, k with Hk == 0.
  *   q_out, k_out  the same shapes with strides of their own; may be q and k themselves with the same
- *                 strides. Other overlaps are not allowed.
+ *                 strides. Other overlaps are not allowed (strides of 0 over several rows are refused).
  *   D             1 .. 1024; any strides. Rows of 16-byte chunks whose pairs keep to chunks (D and all strides
  *                 multiples of 8, rotary_dim of 16 or, interleaved, 8) are moved 16 bytes at a time.
  */

@@ -208,6 +208,13 @@ def _decode(mods=None, **kw):
     return kvq.lib().kvq_decode_kv(*a.values())
 
 
+def test_outputs_whose_rows_coincide_are_refused():
+    for kw in (dict(qot=0), dict(qoh=0), dict(kot=0), dict(koh=0), dict(q=None, Hq=0, qo=None, koh=0)):
+        assert _rope(**kw) == BAD, kw
+    for kw in (dict(qot=0), dict(qoh=0)):
+        assert _write(**kw) == BAD, kw
+
+
 def test_decode_kv_refusals():
     assert _decode(B=0) == OK
     for kw in (dict(B=-1), dict(Hq=0), dict(Hk=0), dict(Hq=5), dict(mb=-1), dict(mb=0), dict(S=-1), dict(cache=None),
