@@ -17,6 +17,9 @@
 // four additions. Before that (places walked lane by lane, angles read from shared memory for each item, a division
 // here and there) the prefill of 16384 tokens was bound by its instructions: 71-76 us, now 65, against a floor of 59.
 // Loading the first rows of q, k and v ahead of the position and the slot costs registers and with them warps: 69 us.
+// Prefetches of a write's rows into L2 cost none and shorten the chain position -> q rows -> k rows -> v rows: 5003 tokens
+// into FP8 14.1 -> 11.5 us, the prefill's pass 67.4 -> 66.4. kvq_rope has no second or third row set behind the first, and
+// the requests run into the loads that follow at once: 8192 tokens of 64 heads 47.8 -> 54.7 us, so it does without.
 //
 // Heads whose pairs do not keep to such chunks (rotary_dim / 2 not a multiple of 8, odd strides, D > 512) take
 // the element path: a thread owns a pair (or one element that passes), so that q_out == q stays safe.
@@ -52,6 +55,7 @@ struct WriteKvParams {
   int32_t T, D;
   int32_t bs_shift;            // log2 of the block size, or -1
   int32_t row_shift;           // chunk path: log2 of the lanes that a row takes
+  int32_t ahead_q, ahead_kv;   // rows of a token that start for L2 ahead of their loads
 };
 
 constexpr int kWriteWarps = 4;  // of a CTA: small ones, so that the last wave is full
@@ -234,6 +238,15 @@ __global__ void __launch_bounds__(32 * kWriteWarps) write_kv_kernel(const WriteK
   const uint8_t *q_src = static_cast<const uint8_t *>(p.q.src) + t * p.q.src_t * EI;
   const uint8_t *k_src = static_cast<const uint8_t *>(p.k.src) + t * p.k.src_t * EI;
   [[maybe_unused]] const uint8_t *v_src = static_cast<const uint8_t *>(p.v.src) + t * p.v.src_t * EI;
+  if constexpr (POOL >= 0) {  // rows on their way to L2 while the angles are computed
+    auto ahead = [&](const uint8_t *src, long long src_h, int rows) {
+      for (int r = 32 * part + lane; r < rows; r += 32 * gridDim.y)
+        for (int b = 0; b < p.D * EI; b += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + r * src_h * EI + b));
+    };
+    ahead(q_src, p.q.src_h, p.ahead_q);
+    ahead(k_src, p.k.src_h, p.ahead_kv);
+    ahead(v_src, p.v.src_h, p.ahead_kv);
+  }
   const int half = rot ? p.half : 0, R = 2 * half;
   // places: pairs of chunks of the rotated part (rc chunks), then of the rest (pc)
   const int lanes = 1 << p.row_shift, j = lane & (lanes - 1);
@@ -492,6 +505,12 @@ extern "C" kvq_status kvq_write_kv(const void *key, int64_t k_stride_t, int64_t 
   p.T = T;
   p.D = D;
   const bool vec = chunked_pairs(p);
+  // Rows of a few tokens are still in L2 from the projection that made them: asking for them there first costs (40 tokens
+  // 2.8 -> 3.2 us, 333 tokens into FP8 3.3 -> 3.7); from 2 MB of rows on it gains (640 tokens 7.0 -> 6.3 us).
+  if (2LL * T * (Hq + 2LL * Hk) * D >= (2 << 20)) {
+    p.ahead_q = Hq;
+    p.ahead_kv = Hk;
+  }
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (cache->dtype == KVQ_E4M3)
     return dtype == KVQ_BF16 ? launch_write_kv<KVQ_BF16, kFp8Dst>(p, vec, s)
